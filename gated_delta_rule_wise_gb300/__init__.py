@@ -31,6 +31,11 @@ __all__ = [
     "KDA_F32", "KDA_BF16", "KDA_ALPHA_NONE", "KDA_ALPHA_SCALAR", "KDA_ALPHA_CHANNEL",
     "KDA_PATH_AUTO", "KDA_PATH_CUDA_CORE", "KDA_PATH_TENSOR", "KDA_PATH_TENSOR_SPLIT_SCAN",
     "KDA_PATH_TENSOR_WIDE_SCAN", "KDA_PATH_TENSOR_PIPELINED",
+    "kda_short_conv", "kda_short_conv_step", "short_conv", "short_conv_step",
+    "kda_selective_scan", "kda_selective_scan_workspace_size", "kda_selective_step",
+    "selective_scan", "selective_scan_workspace_for", "selective_step",
+    "kda_state_copy", "kda_state_clear", "state_copy", "state_clear",
+    "KDA_ACT_NONE", "KDA_ACT_SILU", "KDA_SCAN_SOFTPLUS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +52,7 @@ _lock = threading.Lock()
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_LL = ctypes.c_longlong
 _SZ = ctypes.c_size_t
 
 
@@ -101,6 +107,23 @@ def load_library():
         lib.kda_chunk_fwd_host.argtypes = [_P] * 8 + [_I] * 9 + [_P, _SZ, _P]
         lib.kda_selftest_wait_timeout.restype = _I
         lib.kda_selftest_wait_timeout.argtypes = [_P, _SZ, ctypes.c_uint, _P]
+        lib.kda_short_conv.restype = _I
+        lib.kda_short_conv.argtypes = [_P, _LL, _LL, _LL] + [_P] * 6 + [_I] * 7 + [_P]
+        lib.kda_short_conv_step.restype = _I
+        lib.kda_short_conv_step.argtypes = ([_P, _LL, _LL] + [_P] * 4 + [_I, _P] + [_I] * 6 +
+                                            [_P])
+        lib.kda_selective_scan_workspace_size.restype = _SZ
+        lib.kda_selective_scan_workspace_size.argtypes = [_I] * 6
+        lib.kda_selective_scan.restype = _I
+        lib.kda_selective_scan.argtypes = ([_P] * 12 + [ctypes.POINTER(_LL)] + [_I] * 6 +
+                                           [ctypes.c_uint, _P, _SZ, _P])
+        lib.kda_selective_step.restype = _I
+        lib.kda_selective_step.argtypes = ([_P] * 10 + [_I, _P, ctypes.POINTER(_LL)] + [_I] * 5 +
+                                           [ctypes.c_uint, _P])
+        lib.kda_state_copy.restype = _I
+        lib.kda_state_copy.argtypes = [_P, _I, _LL, _I, _LL, _P, _P, _I, _P]
+        lib.kda_state_clear.restype = _I
+        lib.kda_state_clear.argtypes = [_P, _I, _LL, _I, _LL, _P, _I, _P]
         if lib.kda_abi_version() != ABI_VERSION:
             raise RuntimeError("libkda.so ABI version does not match this binding; rebuild it")
         _lib = lib
@@ -350,3 +373,271 @@ def decode_step(q, k, v, beta, log_alpha, S, stream=None):
     o = torch.empty(v.shape, dtype=q.dtype, device=q.device)
     kda_decode_step(q, k, v, beta, log_alpha, S, o, stream)
     return o
+
+
+# ---------------------------------------------------------------- short convolution, selective scan
+
+KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
+KDA_SCAN_SOFTPLUS = 1
+
+
+def _call(dev, stream, fn, what, *args):
+    """Call ``fn(*args, stream)`` with ``dev`` (the tensors' device) current."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), what)
+
+
+def _keep(stream, *tensors):
+    """Tensors allocated here but used on a stream the caller chose: their
+    memory is not handed out again before that stream has passed the call."""
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _dense(t, name, shape, dtype, dev):
+    """Pointer of a contiguous device tensor of this shape and type; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return _ptr(t)
+
+
+def _strided(t, name, shape, dtype, dev):
+    """Pointer of a device tensor of this shape and type whose last axis is dense."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"libkda takes device tensors: {name} is on {t.device}")
+    return t.device
+
+
+def _group_rows(t, name, shape, dtype, dev):
+    """Pointer of B or C, [..., G, N] with the last two axes dense."""
+    p = _strided(t, name, shape, dtype, dev)
+    if shape[-2] > 1 and t.stride(-2) != shape[-1] and t.numel() > 0:
+        raise ValueError(f"the last two axes of {name} must be contiguous")
+    return p
+
+
+def kda_short_conv(x, w, bias, s0, lens, y, sT, act=KDA_ACT_SILU, stream=None):
+    """Short causal convolution over time through the C ABI.  x [B,H,T,d] (any
+    strides with a dense last axis), w [H,d,W] float32, bias [H,d] float32 or
+    None, s0, sT [B,H,W-1,d] of x's type or None, lens [B] int32 or None,
+    y [B,H,T,d] (written; rows behind a sequence's length are left alone)."""
+    dev, dt = _device_of(x, "x"), x.dtype
+    code = _dtype_code(x)
+    B, H, T, d = x.shape
+    W = w.shape[-1]
+    f32 = torch.float32
+    _call(dev, stream, load_library().kda_short_conv, "kda_short_conv",
+          _strided(x, "x", (B, H, T, d), dt, dev), x.stride(0), x.stride(1), x.stride(2),
+          _dense(w, "w", (H, d, W), f32, dev), _dense(bias, "bias", (H, d), f32, dev),
+          _dense(s0, "s0", (B, H, W - 1, d), dt, dev),
+          _dense(lens, "lens", (B,), torch.int32, dev), _dense(y, "y", (B, H, T, d), dt, dev),
+          _dense(sT, "sT", (B, H, W - 1, d), dt, dev), B, H, T, d, W, code, act)
+
+
+def short_conv(x, w, bias=None, s0=None, lens=None, act=KDA_ACT_SILU, output_final_state=True,
+               out=None, stream=None):
+    """Allocate y (unless ``out`` is given) and sT and run ``kda_short_conv``;
+    returns (y, sT or None).  With ``lens`` the rows of a new y behind a
+    sequence's length hold nothing."""
+    B, H, T, d = x.shape
+    y = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device) if out is None else out
+    sT = (torch.empty((B, H, w.shape[-1] - 1, d), dtype=x.dtype, device=x.device)
+          if output_final_state else None)
+    kda_short_conv(x, w, bias, s0, lens, y, sT, act, stream)
+    _keep(stream, y, sT)
+    return y, sT
+
+
+def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
+    """One token of ``kda_short_conv`` for N sequences, in place.  x [N,H,d]
+    (strided), S [n_slots,H,W-1,d], slots [N] int32 or None (row n uses slot
+    n); rows whose slot is outside the pool are skipped; y [N,H,d]."""
+    dev, dt = _device_of(x, "x"), x.dtype
+    code = _dtype_code(x)
+    N, H, d = x.shape
+    W, P = w.shape[-1], S.shape[0]
+    f32 = torch.float32
+    _call(dev, stream, load_library().kda_short_conv_step, "kda_short_conv_step",
+          _strided(x, "x", (N, H, d), dt, dev), x.stride(0), x.stride(1),
+          _dense(w, "w", (H, d, W), f32, dev), _dense(bias, "bias", (H, d), f32, dev),
+          _dense(S, "S", (P, H, W - 1, d), dt, dev),
+          _dense(slots, "slots", (N,), torch.int32, dev), P,
+          _dense(y, "y", (N, H, d), dt, dev), N, H, d, W, code, act)
+
+
+def short_conv_step(x, w, S, bias=None, slots=None, act=KDA_ACT_SILU, out=None, stream=None):
+    """Allocate y (unless ``out`` is given) and run ``kda_short_conv_step``; returns y."""
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    kda_short_conv_step(x, w, bias, S, slots, y, act, stream)
+    _keep(stream, y)
+    return y
+
+
+def kda_selective_scan_workspace_size(B, T, D, G, N, dtype) -> int:
+    return load_library().kda_selective_scan_workspace_size(B, T, D, G, N, dtype)
+
+
+def selective_scan_workspace_for(u, A, B):
+    """Workspace for ``kda_selective_scan`` on u [B,T,D], A [D,N], B [B,T,G,N]."""
+    n = kda_selective_scan_workspace_size(u.shape[0], u.shape[1], u.shape[2], B.shape[2],
+                                          A.shape[1], _dtype_code(u))
+    if n == 0:
+        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_selective_scan_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=u.device)
+
+
+def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, workspace,
+                       softplus=True, stream=None):
+    """Selective state space scan through the C ABI.  u, delta, z [B,T,D] (z
+    may be None), B, C [B,T,G,N]: strided, one type; A [D,N], D, delta_bias [D]
+    (or None), h0, hT [B,D,N] (or None) float32; lens [B] int32 or None;
+    y [B,T,D] (written; rows behind a sequence's length are left alone)."""
+    dev, dt = _device_of(u, "u"), u.dtype
+    code = _dtype_code(u)
+    nB, T, nD = u.shape
+    G, N = B.shape[2], A.shape[1]
+    f32 = torch.float32
+    st = (_LL * 10)(u.stride(0), u.stride(1), delta.stride(0), delta.stride(1), B.stride(0),
+                    B.stride(1), C.stride(0), C.stride(1),
+                    0 if z is None else z.stride(0), 0 if z is None else z.stride(1))
+    _call(dev, stream, load_library().kda_selective_scan, "kda_selective_scan",
+          _strided(u, "u", (nB, T, nD), dt, dev), _strided(delta, "delta", (nB, T, nD), dt, dev),
+          _dense(A, "A", (nD, N), f32, dev), _group_rows(B, "B", (nB, T, G, N), dt, dev),
+          _group_rows(C, "C", (nB, T, G, N), dt, dev), _dense(D, "D", (nD,), f32, dev),
+          None if z is None else _strided(z, "z", (nB, T, nD), dt, dev),
+          _dense(delta_bias, "delta_bias", (nD,), f32, dev),
+          _dense(h0, "h0", (nB, nD, N), f32, dev), _dense(lens, "lens", (nB,), torch.int32, dev),
+          _dense(y, "y", (nB, T, nD), dt, dev), _dense(hT, "hT", (nB, nD, N), f32, dev),
+          st, nB, T, nD, G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+
+
+def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, lens=None,
+                   softplus=True, output_final_state=True, out=None, stream=None,
+                   workspace=None):
+    """Allocate y (unless ``out`` is given), hT and the workspace and run
+    ``kda_selective_scan``; returns (y, hT or None).  With ``lens`` the rows of
+    a new y behind a sequence's length hold nothing."""
+    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
+    hT = (torch.empty((u.shape[0],) + tuple(A.shape), dtype=torch.float32, device=u.device)
+          if output_final_state else None)
+    ws = selective_scan_workspace_for(u, A, B) if workspace is None else workspace
+    kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, ws, softplus, stream)
+    _keep(stream, y, hT, ws if workspace is None else None)
+    return y, hT
+
+
+def kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplus=True,
+                       stream=None):
+    """One token of ``kda_selective_scan`` for R sequences, in place.  u, delta,
+    z [R,D], B, C [R,G,N] (strided over rows), S [n_slots,D,N] float32, slots
+    as in ``kda_short_conv_step``; y [R,D]."""
+    dev, dt = _device_of(u, "u"), u.dtype
+    code = _dtype_code(u)
+    R, nD = u.shape
+    G, N, P = B.shape[1], A.shape[1], S.shape[0]
+    f32 = torch.float32
+    st = (_LL * 5)(u.stride(0), delta.stride(0), B.stride(0), C.stride(0),
+                   0 if z is None else z.stride(0))
+    _call(dev, stream, load_library().kda_selective_step, "kda_selective_step",
+          _strided(u, "u", (R, nD), dt, dev), _strided(delta, "delta", (R, nD), dt, dev),
+          _dense(A, "A", (nD, N), f32, dev), _group_rows(B, "B", (R, G, N), dt, dev),
+          _group_rows(C, "C", (R, G, N), dt, dev), _dense(D, "D", (nD,), f32, dev),
+          None if z is None else _strided(z, "z", (R, nD), dt, dev),
+          _dense(delta_bias, "delta_bias", (nD,), f32, dev),
+          _dense(S, "S", (P, nD, N), f32, dev), _dense(slots, "slots", (R,), torch.int32, dev), P,
+          _dense(y, "y", (R, nD), dt, dev), st, R, nD, G, N, code,
+          KDA_SCAN_SOFTPLUS if softplus else 0)
+
+
+def selective_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, slots=None,
+                   softplus=True, out=None, stream=None):
+    """Allocate y (unless ``out`` is given) and run ``kda_selective_step``; returns y."""
+    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
+    kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplus, stream)
+    _keep(stream, y)
+    return y
+
+
+# ---------------------------------------------------------------- states in slots
+
+def _index_list(ix, name):
+    """A host list of slot indexes (Python list, or a CPU tensor) as contiguous int32."""
+    if isinstance(ix, torch.Tensor):
+        if ix.is_cuda or ix.dim() != 1 or ix.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"{name} must be a list or a one-dimensional integer CPU tensor")
+        if ix.dtype == torch.int64 and ix.numel() and (ix.min() < -2**31 or ix.max() >= 2**31):
+            raise ValueError(f"{name} holds an index outside 32 bits")
+        return ix.to(torch.int32).contiguous()
+    return torch.tensor(ix, dtype=torch.int32)
+
+
+def _pool_args(pool, layered):
+    """(pointer, layers, layer stride, slots, slot bytes) of a pool [slots, ...]
+    or, ``layered``, [layers, slots, ...] (layers may be strided)."""
+    dev = _device_of(pool, "pool")
+    if pool.dim() < (2 if layered else 1):
+        raise ValueError("pool has too few axes")
+    one = pool[0] if layered and pool.shape[0] else pool
+    if not one.is_contiguous():
+        raise ValueError("the slots of a pool must be contiguous")
+    e = pool.element_size()
+    if not layered:
+        n = pool.shape[0]
+        return dev, pool.data_ptr(), 1, 0, n, (pool.numel() // n * e if n else 0)
+    L, n = pool.shape[0], pool.shape[1]
+    per = pool.numel() // (L * n) * e if L * n else 0
+    return dev, pool.data_ptr(), L, pool.stride(0) * e if L > 1 else 0, n, per
+
+
+def kda_state_copy(pool, src, dst, layered=False, stream=None):
+    """Copy slot ``src[i]`` of ``pool`` to slot ``dst[i]``, in the list's order.
+    pool [slots, ...], or [layers, slots, ...] with ``layered`` (the pair acts in
+    every layer); src, dst: host lists (Python lists or CPU integer tensors)."""
+    dev, *args = _pool_args(pool, layered)
+    a, b = _index_list(src, "src"), _index_list(dst, "dst")
+    if a.numel() != b.numel():
+        raise ValueError("src and dst must have the same length")
+    _call(dev, stream, load_library().kda_state_copy, "kda_state_copy", *args, a.data_ptr(),
+          b.data_ptr(), a.numel())
+
+
+def kda_state_clear(pool, slots, layered=False, stream=None):
+    """Fill the listed slots of ``pool`` (as in ``kda_state_copy``) with zeros."""
+    dev, *args = _pool_args(pool, layered)
+    a = _index_list(slots, "slots")
+    _call(dev, stream, load_library().kda_state_clear, "kda_state_clear", *args, a.data_ptr(),
+          a.numel())
+
+
+def state_copy(pool, src, dst, layered=False, stream=None):
+    """``kda_state_copy``; returns ``pool``."""
+    kda_state_copy(pool, src, dst, layered, stream)
+    return pool
+
+
+def state_clear(pool, slots, layered=False, stream=None):
+    """``kda_state_clear``; returns ``pool``."""
+    kda_state_clear(pool, slots, layered, stream)
+    return pool

@@ -30,7 +30,8 @@
  *    stated; the caller allocates and owns them.  The library allocates no
  *    device memory and keeps no state between calls.
  *  - Every device pointer must be 16-byte aligned; the workspace 256-byte
- *    aligned.  Misaligned pointers return KDA_ERR_INVALID_ARG.
+ *    aligned.  Misaligned pointers return KDA_ERR_INVALID_ARG.  Strided inputs
+ *    and state pools, where a function has them, may start at any element.
  *  - Calls are asynchronous on `stream` (NULL = legacy default stream) and
  *    never synchronise, except kda_chunk_fwd_status.  Arguments are checked
  *    before anything is launched; on an error status nothing was launched.
@@ -361,6 +362,140 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v,
                            float *S_inout, void *o,
                            int N, int H, int dk, int dv,
                            kda_dtype dt, kda_alpha_mode am, kda_stream_t stream);
+
+/*
+ * Short causal convolution: each channel of each head convolved over time with
+ * its own W taps, optionally followed by silu.  It is what the delta-rule and
+ * state-space models put between their input projections and the recurrence
+ * (on q, k, v before kda_chunk_fwd; on u before kda_selective_scan).  With
+ * xx = [s0 ; x] along time,
+ *
+ *   y[b,h,t,i] = act(bias[h,i] + sum_{j<W} w[h,i,j] xx[b,h,t+j,i])
+ *   sT[b,h]    = the last W - 1 rows of xx[b,h, 0 : W-1+len_b]
+ *
+ *   x     [B, H, T, d]    dtype dt, strided: element (b,h,t,i) is
+ *                         x[b x_sb + h x_sh + t x_st + i]; strides >= 0 in
+ *                         elements.  Takes a projection's output (token by
+ *                         token, or one slice of it) as it is
+ *   w     [H, d, W]       float32; w[.., W-1] meets the current token
+ *   bias  [H, d]          float32, or NULL for 0
+ *   s0    [B, H, W-1, d]  dtype dt, the W - 1 inputs before the call, oldest
+ *                         first, or NULL for zeros
+ *   lens  [B]             int32 (device), or NULL: row b has lens[b] tokens
+ *                         (clamped to [0, T]); tokens behind them are not read
+ *                         and their rows of y are left as they were
+ *   y     [B, H, T, d]    dtype dt, contiguous (written; must not overlap x)
+ *   sT    [B, H, W-1, d]  dtype dt, or NULL (written; may equal s0)
+ *   W in {2, 3, 4}, else KDA_ERR_UNSUPPORTED; any d >= 1.  Sums in float32,
+ *   rounded once.  x needs only its element's alignment; 16-byte aligned rows
+ *   (pointer and strides) are read with wide loads.
+ */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_act;
+kda_status kda_short_conv(const void *x, long long x_sb, long long x_sh, long long x_st,
+                          const float *w, const float *bias, const void *s0, const int *lens,
+                          void *y, void *sT, int B, int H, int T, int d, int W, kda_dtype dt,
+                          kda_act act, kda_stream_t stream);
+
+/*
+ * One token of the same convolution for N sequences, states updated in place
+ * in a pool of slots:
+ *
+ *   x      [N, H, d]            dtype dt, strided (x_sn, x_sh)
+ *   S      [n_slots, H, W-1, d] dtype dt (read, shifted by one, written)
+ *   slots  [N] int32 (device), or NULL: row n uses slot slots[n] (NULL: slot
+ *          n, and N <= n_slots).  A row whose index is outside [0, n_slots) is
+ *          skipped: its y and every slot stay as they were (padding rows of a
+ *          captured batch use -1).  Rows that are not skipped must name
+ *          different slots; the results of rows that share one are undefined
+ *   y      [N, H, d]            dtype dt, contiguous (written)
+ */
+kda_status kda_short_conv_step(const void *x, long long x_sn, long long x_sh, const float *w,
+                               const float *bias, void *S, const int *slots, int n_slots, void *y,
+                               int N, int H, int d, int W, kda_dtype dt, kda_act act,
+                               kda_stream_t stream);
+
+/*
+ * Selective state space scan over T tokens: a diagonal recurrence whose decay
+ * belongs to every (channel, state) entry, where the gated delta rule's
+ * belongs to a row of a head's state.  Per batch row b, channel c of group
+ * g = c / (D / G), state entry n:
+ *
+ *   dt_t   = delta_t[c] + delta_bias[c], through softplus(x) = log(1 + exp(x))
+ *            when KDA_SCAN_SOFTPLUS is set
+ *   h[c,n] = exp(dt_t A[c,n]) h[c,n] + dt_t u_t[c] B_t[g,n]
+ *   y_t[c] = (sum_n C_t[g,n] h[c,n] + Dskip[c] u_t[c]) silu(z_t[c])
+ *
+ *   u, delta, z [B, T, D]     dtype dt, strided; z NULL: no gate
+ *   A           [D, N]        float32 (negative entries decay)
+ *   Bm, Cm      [B, T, G, N]  dtype dt, strided over b and t
+ *   Dskip, delta_bias [D]     float32, or NULL for 0
+ *   h0          [B, D, N]     float32, or NULL for zeros
+ *   lens        [B]           int32 (device), or NULL, as in kda_short_conv
+ *   y           [B, T, D]     dtype dt, contiguous (written)
+ *   hT          [B, D, N]     float32, or NULL (written; may equal h0)
+ *   strides     10 element strides in HOST memory, each >= 0: batch and token
+ *               stride of u, delta, Bm, Cm and z in this order (those of z are
+ *               not read when z is NULL)
+ *   N in {8, 16, 32, 64}, G >= 1 divides D; else KDA_ERR_UNSUPPORTED /
+ *   KDA_ERR_INVALID_ARG.
+ *   workspace   >= kda_selective_scan_workspace_size(...) bytes of device
+ *               memory, 256-byte aligned, not shared with a concurrent call;
+ *               it needs no initialisation.
+ *
+ * State and sums in float32; y rounded once.  The strided inputs need only
+ * their element's alignment.
+ */
+#define KDA_SCAN_SOFTPLUS 1u
+size_t kda_selective_scan_workspace_size(int B, int T, int D, int G, int N, kda_dtype dt);
+kda_status kda_selective_scan(const void *u, const void *delta, const float *A, const void *Bm,
+                              const void *Cm, const float *Dskip, const void *z,
+                              const float *delta_bias, const float *h0, const int *lens, void *y,
+                              float *hT, const long long *strides, int B, int T, int D, int G,
+                              int N, kda_dtype dt, unsigned flags, void *workspace,
+                              size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * One token of the same scan for R sequences, states updated in place in a
+ * pool of slots (slots as in kda_short_conv_step):
+ *
+ *   u, delta, z [R, D]; Bm, Cm [R, G, N]  dtype dt, strided over rows: strides
+ *               holds 5 row strides, of u, delta, Bm, Cm and z
+ *   S           [n_slots, D, N] float32 (read and written)
+ *   y           [R, D]          dtype dt, contiguous (written)
+ */
+kda_status kda_selective_step(const void *u, const void *delta, const float *A, const void *Bm,
+                              const void *Cm, const float *Dskip, const void *z,
+                              const float *delta_bias, float *S, const int *slots, int n_slots,
+                              void *y, const long long *strides, int R, int D, int G, int N,
+                              kda_dtype dt, unsigned flags, kda_stream_t stream);
+
+/*
+ * Copies and clears of whole states in a pool, the bookkeeping of a cache
+ * whose pages are the fixed-size states of these recurrences: moving live
+ * sequences into the slots of ended ones, forking a sequence (one source,
+ * several destinations), clearing the slots of new ones.  The pool holds
+ * `layers` layers, layer_stride bytes apart, of n_slots slots of slot_bytes
+ * each; a pair acts on its two slots in every layer.
+ *
+ *   src, dst, slots   int32 lists in HOST memory; read before the call
+ *                     returns, every index in [0, n_slots), else
+ *                     KDA_ERR_INVALID_ARG
+ *
+ * kda_state_copy: slot dst[i] receives slot src[i], for i = 0 .. n-1 with the
+ * effect of that order: a pair may read what an earlier one wrote, and a slot
+ * may occur any number of times on either side.  src[i] == dst[i] does
+ * nothing.  Lists in which no pair touches what another writes (forks, moves
+ * into free slots) run all at once.
+ * kda_state_clear: the listed slots are filled with zero bytes.
+ * layers, n_slots, n >= 0; slot_bytes >= 0; layer_stride >= n_slots *
+ * slot_bytes where layers > 1.  The pool needs no alignment beyond its element;
+ * 16-byte aligned pools, strides and slots move in 16-byte pieces.
+ */
+kda_status kda_state_copy(void *pool, int layers, long long layer_stride, int n_slots,
+                          long long slot_bytes, const int *src, const int *dst, int n,
+                          kda_stream_t stream);
+kda_status kda_state_clear(void *pool, int layers, long long layer_stride, int n_slots,
+                           long long slot_bytes, const int *slots, int n, kda_stream_t stream);
 
 /*
  * Device self-test of the bounded-wait mechanism: launches one block that

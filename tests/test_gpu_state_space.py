@@ -1,0 +1,513 @@
+"""Short causal convolution, selective scan, their single-token forms and the
+slot copies on the GPU, against float64 definitions within derived bounds."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_wise_gb300 as kda
+from _state_space import (conv_bound, conv_case, dev, host, scan_bound, scan_case, store, within)
+from oracle import state_space as O
+
+pytestmark = pytest.mark.gpu
+ACT = {"silu": kda.KDA_ACT_SILU, "none": kda.KDA_ACT_NONE}
+MARK = 7.25  # exact in bf16: what rows that a call must leave alone hold
+
+
+def _run_conv(c, dtype, act, layout="heads", inplace=False):
+    """layout: "heads" [B,H,T,d]; "tokens" a transposed [B,T,H,d]; "slice" one
+    that starts one element into a wider projection."""
+    x = dev(c["x"], dtype)
+    B, H, T, d = x.shape
+    if layout != "heads":
+        pad = 0 if layout == "tokens" else 3
+        base = torch.full((B, T, H, d + pad), float("nan"), dtype=x.dtype, device=x.device)
+        base[..., pad // 3:pad // 3 + d] = x.transpose(1, 2)
+        x = base[..., pad // 3:pad // 3 + d].transpose(1, 2)
+    y = torch.full((B, H, T, d), MARK, dtype=x.dtype, device=x.device)
+    s0 = dev(c["s0"], dtype)
+    w, bias, lens = dev(c["w"]), dev(c["bias"]), dev(c["lens"])
+    if inplace:
+        kda.kda_short_conv(x, w, bias, s0, lens, y, s0, ACT[act])
+        sT = s0
+    else:
+        y, sT = kda.short_conv(x, w, bias, s0, lens, ACT[act], out=y)
+    torch.cuda.synchronize()
+    return host(y), host(sT)
+
+
+def _check_conv(c, dtype, act, **kw):
+    y, sT = _run_conv(c, dtype, act, **kw)
+    ref, sref = O.short_conv(c["x"], c["w"], c["bias"], c["s0"], c["lens"], act)
+    within(y, ref, conv_bound(c["x"], c["w"], c["bias"], c["s0"], c["lens"], act, dtype, ref), "y")
+    assert (y[np.isnan(ref)] == MARK).all()
+    assert np.array_equal(sT, sref)
+
+
+@pytest.mark.parametrize("W_", [2, 3, 4])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,T,d", [(1, 1, 1, 1), (2, 3, 2, 8), (1, 2, 33, 128), (2, 1, 65, 130),
+                                     (3, 2, 130, 12), (1, 1, 700, 257), (1, 5, 515, 64)])
+def test_conv_sizes(B, H, T, d, W_, dtype):
+    layout = ["heads", "tokens", "slice"][(T + W_) % 3]
+    _check_conv(conv_case(T + d + W_, B, H, T, d, W_, dtype, bias=T % 2 == 0, state=d % 2 == 0),
+                dtype, "silu" if T % 3 else "none", layout=layout)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "slice"])
+@pytest.mark.parametrize("d", [24, 31])
+def test_conv_padded_batch(dtype, layout, d):
+    """Lengths 0, 1, 2, in the middle, full, and outside [0, T]; the padding holds NaN."""
+    lens = [0, 1, 2, 37, 100, 250, -3]
+    c = conv_case(5, len(lens), 2, 100, d, 4, dtype, bias=True, state=True, lens=lens)
+    for b, n in enumerate(lens):
+        c["x"][b, :, max(n, 0):] = np.nan
+    _check_conv(c, dtype, "silu", layout=layout, inplace=layout == "tokens")
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 3, 40, 1000])
+def test_conv_state_in_place(T):
+    _check_conv(conv_case(T, 2, 2, T, 40, 4, "bf16", state=True), "bf16", "silu", inplace=True)
+
+
+def test_conv_many_tokens_few_channels():
+    _check_conv(conv_case(9, 1, 1, 20011, 3, 4, "f32"), "f32", "silu")
+
+
+def test_conv_special_values():
+    """Infinities and NaN reach exactly the W tokens that see them; large
+    negative sums give zero, large positive ones themselves."""
+    c = conv_case(3, 1, 1, 40, 16, 4, "f32")
+    c["x"][0, 0, 10, 3] = np.nan
+    c["w"][0, 5] = [0, 0, 0, 1]
+    c["x"][0, 0, 20:24, 5] = [-1e4, -200.0, 200.0, 1e30]
+    y, _ = _run_conv(c, "f32", "silu")
+    assert np.isnan(y[0, 0, 10:14, 3]).all() and np.isnan(y).sum() == 4
+    assert np.allclose(y[0, 0, 20:24, 5], [0, 0, 200, 1e30], rtol=1e-6, atol=1e-30)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,H,d,W_", [(1, 1, 1, 2), (3, 2, 8, 4), (9, 1, 130, 3), (40, 4, 128, 4),
+                                      (300, 2, 24, 4)])
+def test_conv_step(N, H, d, W_, dtype):
+    """Rows in scattered slots, one skipped by -1, one by an index past the
+    pool; slots no row names keep their bits.  Two tokens."""
+    r = np.random.default_rng(N + d)
+    c = conv_case(N, N, H, 2, d, W_, dtype, bias=True)
+    P = N + 3
+    slots = r.permutation(P)[:N].astype(np.int32)
+    if N > 2:
+        slots[1], slots[2] = -1, P
+    pool = store(r.standard_normal((P, H, W_ - 1, d)), dtype)
+    S, y = dev(pool, dtype), None
+    want = pool.astype(np.float64)
+    for t in range(2):
+        wide = torch.full((N, H, d + 5), float("nan"), device="cuda",
+                          dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+        wide[..., 1:1 + d] = dev(c["x"][:, :, t], dtype)
+        y = torch.full((N, H, d), MARK, dtype=wide.dtype, device="cuda")
+        kda.short_conv_step(wide[..., 1:1 + d], dev(c["w"]), S, dev(c["bias"]), dev(slots), out=y)
+        torch.cuda.synchronize()
+        got = host(y)
+        for n, s in enumerate(slots):
+            if not 0 <= s < P:
+                assert (got[n] == MARK).all()
+                continue
+            x1 = c["x"][n:n + 1, :, t:t + 1]
+            ref, sT = O.short_conv(x1, c["w"], c["bias"], want[s][None], None, "silu")
+            b = conv_bound(x1, c["w"], c["bias"], want[s][None], None, "silu", dtype, ref)
+            within(got[n], ref[0, :, 0], b[0, :, 0], f"row {n}")
+            want[s] = sT[0]
+        assert np.array_equal(host(S), want)
+
+
+def test_conv_step_without_slots():
+    c = conv_case(1, 5, 2, 1, 16, 4, "bf16", state=True)
+    S = dev(c["s0"], "bf16")
+    y = kda.short_conv_step(dev(c["x"][:, :, 0], "bf16"), dev(c["w"]), S)
+    ref, sT = O.short_conv(c["x"], c["w"], None, c["s0"])
+    within(host(y)[:, :, None], ref, conv_bound(c["x"], c["w"], None, c["s0"], None, "silu",
+                                                "bf16", ref))
+    assert np.array_equal(host(S), sT)
+
+
+# ---------------------------------------------------------------- selective scan
+
+def _scan_tensors(c, dtype, strided):
+    t = {k: dev(c[k], dtype) for k in ("u", "delta", "Bm", "Cm", "z")}
+    if strided:  # slices of wider rows, from an odd element on, NaN around them
+        for k, v in t.items():
+            if v is None:
+                continue
+            flat = v.flatten(2)
+            wide = torch.full(flat.shape[:2] + (flat.shape[2] + 5,), float("nan"), dtype=v.dtype,
+                              device="cuda")
+            wide[..., 3:3 + flat.shape[2]] = flat
+            t[k] = wide[..., 3:3 + flat.shape[2]].unflatten(2, v.shape[2:])
+    t.update({k: dev(c[k]) for k in ("A", "D", "delta_bias", "h0", "lens")})
+    return t
+
+
+def _check_scan(c, dtype, use_softplus=True, strided=False, inplace=False, **kw):
+    t = _scan_tensors(c, dtype, strided)
+    y = torch.full(t["u"].shape, MARK, dtype=t["u"].dtype, device="cuda")
+    if inplace:
+        hT = t["h0"]
+        kda.kda_selective_scan(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"],
+                               t["delta_bias"], t["h0"], t["lens"], y, hT,
+                               kda.selective_scan_workspace_for(t["u"], t["A"], t["Bm"]),
+                               use_softplus)
+    else:
+        y, hT = kda.selective_scan(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"],
+                                   t["delta_bias"], t["h0"], t["lens"], use_softplus, out=y, **kw)
+    torch.cuda.synchronize()
+    yb, hb, ref, href = scan_bound(c["u"], c["delta"], c["A"], c["Bm"], c["Cm"], c["D"], c["z"],
+                                   c["delta_bias"], c["h0"], c["lens"], use_softplus, dtype)
+    got = host(y)
+    within(got, ref, yb, "y")
+    assert (got[np.isnan(ref)] == MARK).all()
+    within(host(hT), href, hb, "hT")
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D,G", [(1, 1, 1, 1), (2, 2, 8, 2), (1, 31, 24, 1), (1, 64, 130, 2),
+                                     (3, 65, 36, 3), (2, 200, 40, 1)])
+def test_scan_sizes(B, T, D, G, N, dtype):
+    _check_scan(scan_case(T + N, B, T, D, G, N, dtype, gate=T % 2 == 0, state=D % 3 == 0,
+                          skip=T != 64), dtype, strided=(T + N) % 3 == 0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("T", [100, 700])
+def test_scan_padded_batch(dtype, strided, T):
+    """Lengths 0, 1, in the middle, full, outside [0, T]; the padding holds NaN."""
+    lens = [0, 1, 33, 64, T, T + 9, -1]
+    c = scan_case(4, len(lens), T, 48, 2, 16, dtype, state=True, lens=lens)
+    for b, n in enumerate(lens):
+        for k in ("u", "delta", "Bm", "Cm", "z"):
+            c[k][b, max(n, 0):] = np.nan
+    _check_scan(c, dtype, strided=strided, inplace=strided)
+
+
+@pytest.mark.parametrize("use_softplus,gate,bias,skip", [(False, False, False, False),
+                                                        (False, True, True, True),
+                                                        (True, False, False, True),
+                                                        (True, True, False, False)])
+def test_scan_options(use_softplus, gate, bias, skip):
+    c = scan_case(8, 2, 90, 20, 1, 16, "f32", gate=gate, bias=bias, skip=skip,
+                  use_softplus=use_softplus)
+    _check_scan(c, "f32", use_softplus)
+    _check_scan(c, "f32", use_softplus, output_final_state=True)
+
+
+@pytest.mark.parametrize("T", [0, 1, 50, 900])
+def test_scan_state_in_place(T):
+    _check_scan(scan_case(T, 2, T, 64, 1, 16, "bf16", state=True), "bf16", inplace=True)
+
+
+@pytest.mark.parametrize("B,T,D,G,N,dtype", [(1, 4099, 32, 1, 16, "bf16"), (1, 2500, 7, 1, 8, "f32"),
+                                             (2, 1500, 20, 2, 64, "f32"), (1, 3001, 64, 1, 32, "bf16")])
+def test_scan_long(B, T, D, G, N, dtype):
+    """Few channels and many tokens, the last lengths odd."""
+    _check_scan(scan_case(T, B, T, D, G, N, dtype, state=True), dtype)
+
+
+def test_scan_long_padded():
+    T = 3000
+    _check_scan(scan_case(3, 3, T, 16, 1, 16, "bf16", state=True, lens=[5, 1777, T]), "bf16")
+
+
+def test_scan_strong_decay_and_large_steps():
+    """Steps large enough that exp(dt A) is zero in float32, and softplus
+    arguments where softplus(x) = x and where it is exp(x)."""
+    c = scan_case(6, 1, 60, 16, 1, 16, "f32", bias=False)
+    c["delta"] = np.random.default_rng(0).uniform(-30, 60, c["delta"].shape).astype(np.float32)
+    _check_scan(c, "f32")
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("R,D,G", [(1, 1, 1), (3, 10, 2), (9, 130, 1), (33, 64, 4)])
+def test_step(R, D, G, N, dtype):
+    """Scattered slots, rows skipped by -1 and by an index past the pool,
+    untouched slots keep their bits.  Two tokens."""
+    r = np.random.default_rng(R + N)
+    P = R + 2
+    c = scan_case(R + D, R, 2, D, G, N, dtype)
+    slots = r.permutation(P)[:R].astype(np.int32)
+    if R > 2:
+        slots[0], slots[2] = P + 5, -7
+    pool = (0.5 * r.standard_normal((P, D, N))).astype(np.float32)
+    S = dev(pool)
+    for t in range(2):
+        now = {k: np.ascontiguousarray(c[k][:, t:t + 1]) for k in ("u", "delta", "Bm", "Cm", "z")}
+        x = {k: v[:, 0] for k, v in _scan_tensors({**c, **now}, dtype, D % 2 == 0).items()
+             if k in now}
+        y = torch.full((R, D), MARK, dtype=x["u"].dtype, device="cuda")
+        before = host(S)
+        kda.selective_step(x["u"], x["delta"], dev(c["A"]), x["Bm"], x["Cm"], S, dev(c["D"]),
+                           x["z"], dev(c["delta_bias"]), dev(slots), out=y)
+        torch.cuda.synchronize()
+        after, got, live = host(S), host(y), np.zeros(P, bool)
+        for n, s in enumerate(slots):
+            if not 0 <= s < P:
+                assert (got[n] == MARK).all()
+                continue
+            live[s] = True
+            one = {k: v[n:n + 1] for k, v in now.items()}
+            yb, hb, ref, href = scan_bound(one["u"], one["delta"], c["A"], one["Bm"], one["Cm"],
+                                           c["D"], one["z"], c["delta_bias"], before[s][None],
+                                           None, True, dtype)
+            within(got[n], ref[0, 0], yb[0, 0], f"row {n}")
+            within(after[s], href[0], hb[0], f"slot {s}")
+        assert np.array_equal(after[~live], before[~live])
+
+
+# ---------------------------------------------------------------- states in slots
+
+@pytest.mark.parametrize("shape,dtype,layered", [
+    ((9, 33), torch.bfloat16, False), ((9, 7), torch.uint8, False), ((3, 9, 64), torch.float32, True),
+    ((2, 9, 5, 1000), torch.bfloat16, True), ((9, 2, 40000), torch.float32, False),
+    ((600, 24), torch.float32, False)])
+def test_state_copy_orders(shape, dtype, layered):
+    """Random lists: chains, overwritten destinations, shared sources, no-ops,
+    swaps through a spare slot, more pairs than one launch takes."""
+    r = np.random.default_rng(len(shape) + shape[0])
+    P = shape[1] if layered else shape[0]
+    base = torch.from_numpy(r.integers(0, 100, shape)).to(dtype).cuda()
+    for n in (0, 1, 2, 5, P, 3 * P):
+        for src, dst in ((r.integers(0, P, n), r.integers(0, P, n)),
+                         (r.permutation(P)[:n] % P, r.permutation(P)[:n] % P)):
+            src, dst = src[:len(dst)].tolist(), dst[:len(src)].tolist()
+            pool = base.clone()
+            assert kda.state_copy(pool, src, dst, layered) is pool
+            b = base.float().cpu().numpy()
+            want = O.state_copy(b if layered else b[None], src, dst)
+            assert np.array_equal(pool.float().cpu().numpy(), want if layered else want[0])
+
+
+def test_state_copy_shift_fork_and_index_types():
+    pool = torch.arange(8.0, device="cuda")[:, None].repeat(1, 4).contiguous()
+    kda.state_copy(pool, torch.arange(1, 8), torch.arange(0, 7, dtype=torch.int32))  # shift by one
+    assert pool[:, 0].tolist() == [1, 2, 3, 4, 5, 6, 7, 7]
+    kda.state_copy(pool, [2] * 4, [0, 1, 4, 7])                                      # fork
+    assert pool[:, 0].tolist() == [3, 3, 3, 4, 3, 6, 7, 3]
+
+
+@pytest.mark.parametrize("shape,dtype,layered", [((700, 5), torch.bfloat16, False),
+                                                 ((2, 9, 1024), torch.float32, True)])
+def test_state_clear(shape, dtype, layered):
+    pool = torch.ones(shape, dtype=dtype, device="cuda")
+    P = shape[1] if layered else shape[0]
+    gone = list(range(0, P, 2)) + [0]
+    kda.state_clear(pool, gone, layered)
+    keep = torch.ones(P, dtype=torch.bool)
+    keep[gone] = False
+    v = pool if layered else pool[None]
+    assert (v[:, ~keep.cuda()] == 0).all() and (v[:, keep.cuda()] == 1).all()
+
+
+def test_state_copy_strided_layers():
+    """Layers of a pool that lie further apart than their slots need."""
+    wide = torch.arange(3 * 7 * 10, device="cuda", dtype=torch.float32).view(3, 7, 10)
+    pool = wide[:, :5]
+    want = wide.clone()
+    want[:, 4] = want[:, 0]
+    kda.state_copy(pool, [0], [4], layered=True)
+    assert torch.equal(wide, want)
+
+
+# ---------------------------------------------------------------- as they are used together
+
+def _block(c, dtype, w, bias, stream=None):
+    """Prompt through convolution and scan, as a mixer runs it."""
+    x = dev(c["u"], dtype)[:, None]  # [B, 1, T, D]
+    u, conv = kda.short_conv(x, w, bias, stream=stream)
+    t = _scan_tensors(c, dtype, False)
+    y, h = kda.selective_scan(u[:, 0], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"],
+                              t["delta_bias"], stream=stream)
+    return y, conv, h
+
+
+def test_prompt_then_tokens_then_fork():
+    """Prompts of a batch fill slots; tokens step there; one sequence is
+    forked, another moved, a third slot cleared and started anew; every output
+    agrees with the definition over the whole history."""
+    dtype, B, T, extra, D, N = "f32", 3, 37, 6, 40, 16
+    c = scan_case(21, B, T + extra, D, 1, N, dtype)
+    r = np.random.default_rng(2)
+    w = (0.5 * r.standard_normal((1, D, 4))).astype(np.float32)
+    bias = (0.2 * r.standard_normal((1, D))).astype(np.float32)
+    P = 8
+    part = {k: (v[:, :T] if k in ("u", "delta", "Bm", "Cm", "z") else v) for k, v in c.items()}
+    y, conv, h = _block(part, dtype, dev(w), dev(bias))
+    conv_pool = torch.full((P, 1, 3, D), 9.0, device="cuda")
+    h_pool = torch.full((P, D, N), 9.0, device="cuda")
+    at = [6, 1, 3]
+    conv_pool[at], h_pool[at] = conv, h
+    u_ref, _ = O.short_conv(c["u"][:, None], w, bias)
+    outs = [y]
+    for t in range(T, T + extra):
+        if t == T + 2:  # sequence 1 moves from slot 1 to 0, sequence 2 is forked to 5
+            for pool in (conv_pool, h_pool):
+                kda.state_copy(pool, [1, 3], [0, 5])
+                kda.state_clear(pool, [1])
+            at = [6, 0, 5]
+        slots = dev(np.asarray(at + [-1], np.int32))
+        row = lambda k: torch.cat([dev(c[k][:, t], dtype), torch.full(  # noqa: E731
+            (1,) + c[k].shape[2:], float("nan"), device="cuda")])
+        u = kda.short_conv_step(row("u")[:, None], dev(w), conv_pool, dev(bias), slots)
+        s = kda.selective_step(u[:, 0], row("delta"), dev(c["A"]), row("Bm"), row("Cm"), h_pool,
+                               dev(c["D"]), row("z"), dev(c["delta_bias"]), slots)
+        outs.append(s[:B, None])
+    got = host(torch.cat(outs, 1))
+    assert (h_pool[1] == 0).all() and (conv_pool[1] == 0).all()
+    ref, href = O.selective_scan(u_ref[:, 0], c["delta"], c["A"], c["Bm"], c["Cm"], c["D"], c["z"],
+                                 c["delta_bias"])
+    # u is off by the convolution's bound: at most 2^-20 of its largest value here; the outputs
+    # are sums of N + 1 terms linear in u, so 2^-17 of the largest output holds with room
+    assert np.abs(got - ref).max() <= 2.0 ** -17 * np.abs(ref).max()
+    assert np.abs(host(h_pool[at]) - href).max() <= 2.0 ** -17 * np.abs(href).max()
+
+
+def test_conv_feeds_the_delta_rule():
+    """q, k, v as a projection leaves them, through the convolution into the
+    chunked prefill: the same bits as from contiguous copies of its outputs."""
+    B, T, H, d = 1, 150, 2, 64
+    qkv = torch.randn((B, T, 3 * H * d), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    qkv = qkv.to(torch.bfloat16)
+    w = torch.randn((3, H, d, 4), device="cuda") * 0.5
+    parts = [kda.short_conv(p.unflatten(2, (H, d)).transpose(1, 2), w[i])[0]
+             for i, p in enumerate(qkv.split(H * d, dim=2))]
+    q, k = (torch.nn.functional.normalize(p.float(), dim=-1).to(torch.bfloat16) for p in parts[:2])
+    beta = torch.rand((B, H, T), device="cuda")
+    o, hT = kda.chunk_fwd(q, k, parts[2], beta)
+    torch.cuda.synchronize()
+    import oracle
+    o_ref, _ = oracle.recurrent_heads(host(q), host(k), host(parts[2]), host(beta))
+    got = host(o).reshape(o_ref.shape)
+    assert np.abs(got - o_ref).max() <= 2e-2 * np.abs(o_ref).max()
+    # and the convolution itself
+    x = host(qkv[:, :, :H * d].unflatten(2, (H, d)).transpose(1, 2))
+    ref, _ = O.short_conv(x, host(w[0]))
+    within(host(parts[0]), ref, conv_bound(x, host(w[0]), None, None, None, "silu", "bf16", ref))
+
+
+def test_capture_and_replay_and_other_stream():
+    """One decode step captured into a graph and replayed on new inputs gives
+    the bits of eager calls; a prompt on a side stream gives those of the
+    current one."""
+    D, N, R, P = 72, 16, 5, 8
+    c = scan_case(31, R, 4, D, 1, N, "bf16")
+    w, A, Dk, db = dev(np.full((1, D, 4), 0.3, np.float32)), dev(c["A"]), dev(c["D"]), \
+        dev(c["delta_bias"])
+    slots = torch.tensor([4, 0, 7, -1, 2], dtype=torch.int32, device="cuda")
+    rows = {k: dev(c[k], "bf16") for k in ("u", "delta", "Bm", "Cm", "z")}
+    buf = {k: v[:, 0].clone() for k, v in rows.items()}
+
+    def pools():
+        return torch.zeros((P, 1, 3, D), dtype=torch.bfloat16, device="cuda"), \
+            torch.zeros((P, D, N), device="cuda")
+
+    def step(cp, hp):
+        u = kda.short_conv_step(buf["u"][:, None], w, cp, None, slots, out=mid)
+        kda.selective_step(u[:, 0], buf["delta"], A, buf["Bm"], buf["Cm"], hp, Dk, buf["z"], db,
+                           slots, out=y)
+        kda.state_copy(hp, [4], [1])
+
+    mid = torch.zeros((R, 1, D), dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros((R, D), dtype=torch.bfloat16, device="cuda")
+    cp, hp = pools()
+    want = []
+    for t in range(4):
+        for k in buf:
+            buf[k].copy_(rows[k][:, t])
+        step(cp, hp)
+        want.append((y.clone(), hp.clone()))
+    cp, hp = pools()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(cp, hp)
+    cp.zero_(), hp.zero_()
+    for t in range(4):
+        for k in buf:
+            buf[k].copy_(rows[k][:, t])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[t][0]) and torch.equal(hp, want[t][1]), t
+
+    big = scan_case(32, 1, 2000, 64, 1, 16, "bf16")
+    first = _block(big, "bf16", dev(np.full((1, 64, 4), 0.2, np.float32)), None)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        second = _block(big, "bf16", dev(np.full((1, 64, 4), 0.2, np.float32)), None)
+    side.synchronize()
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+
+
+def test_scan_captured_and_replayed():
+    c = scan_case(33, 2, 1500, 64, 1, 16, "bf16", state=True)
+    t = _scan_tensors(c, "bf16", False)
+    args = (t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"], t["delta_bias"], t["h0"])
+    want = kda.selective_scan(*args)
+    ws = kda.selective_scan_workspace_for(t["u"], t["A"], t["Bm"])
+    out = torch.zeros_like(want[0])
+    kda.selective_scan(*args, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = kda.selective_scan(*args, out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------- refusals of the binding
+
+def test_binding_refuses():
+    x = torch.zeros((1, 2, 4, 8), device="cuda")
+    w = torch.zeros((2, 8, 4), device="cuda")
+    bad = [lambda: kda.short_conv(x, w[:1]), lambda: kda.short_conv(x, w.bfloat16()),
+           lambda: kda.short_conv(x.half(), w), lambda: kda.short_conv(x.cpu(), w),
+           lambda: kda.short_conv(x, w.cpu()),
+           lambda: kda.short_conv(x.transpose(2, 3), torch.zeros((2, 4, 4), device="cuda")),
+           lambda: kda.short_conv(x, w, s0=torch.zeros((1, 2, 2, 8), device="cuda")),
+           lambda: kda.short_conv(x, w, lens=torch.zeros(1, device="cuda")),
+           lambda: kda.short_conv(x, w, out=torch.zeros((1, 2, 4, 8), device="cuda")[..., ::1]
+                                  .transpose(1, 2)),
+           lambda: kda.state_copy(torch.zeros((4, 8), device="cuda"), [0], [1, 2]),
+           lambda: kda.state_copy(torch.zeros((4, 8), device="cuda").t(), [0], [1]),
+           lambda: kda.state_copy(torch.zeros((4, 8)), [0], [1]),
+           lambda: kda.state_copy(torch.zeros((4, 8), device="cuda"),
+                                  torch.zeros(1, dtype=torch.int32, device="cuda"), [1])]
+    c = scan_case(1, 1, 4, 8, 1, 16, "f32")
+    t = _scan_tensors(c, "f32", False)
+    ok = [t[k] for k in ("u", "delta", "A", "Bm", "Cm")]
+    for i, v in enumerate([t["u"][..., :4], t["delta"].bfloat16(), t["A"][:4],
+                           t["Bm"].transpose(1, 2), t["Cm"].cpu()]):
+        a = list(ok)
+        a[i] = v
+        bad.append(lambda a=a: kda.selective_scan(*a))
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was not refused")
+    for src, dst in (([4], [0]), ([0], [-1])):
+        with pytest.raises(kda.KdaError) as e:
+            kda.state_copy(torch.zeros((4, 8), device="cuda"), src, dst)
+        assert e.value.status == kda.KDA_ERR_INVALID_ARG
+    with pytest.raises(kda.KdaError) as e:
+        kda.short_conv(x, torch.zeros((2, 8, 5), device="cuda"))
+    assert e.value.status == kda.KDA_ERR_UNSUPPORTED
+    with pytest.raises(kda.KdaError) as e:
+        kda.short_conv_step(torch.zeros((3, 2, 8), device="cuda"), w,
+                            torch.zeros((2, 2, 3, 8), device="cuda"))
+    assert e.value.status == kda.KDA_ERR_INVALID_ARG  # more rows than slots

@@ -1,0 +1,193 @@
+"""Short convolution, selective scan and slot copies without a GPU: the float64
+definitions against closed forms and each other, the host-side checks of the C
+functions (the pointers here are never dereferenced) and the binding's."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import state_space as O
+
+FAKE = 0x7f0000000000
+INV, UNS, OK = 1, 2, 0
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from gated_delta_rule_wise_gb300 import build
+    build.build()
+    import gated_delta_rule_wise_gb300 as kda
+    return kda.load_library()
+
+
+def test_conv_definition_matches_torch_conv1d():
+    r = np.random.default_rng(0)
+    x, w, b = r.standard_normal((2, 3, 20, 5)), r.standard_normal((3, 5, 4)), r.standard_normal((3, 5))
+    y, sT = O.short_conv(x, w, b, act="silu")
+    xt = torch.from_numpy(x).permute(0, 1, 3, 2).reshape(2, 15, 20)
+    ref = torch.nn.functional.conv1d(torch.nn.functional.pad(xt, (3, 0)),
+                                     torch.from_numpy(w).reshape(15, 1, 4),
+                                     torch.from_numpy(b).reshape(15), groups=15)
+    ref = torch.nn.functional.silu(ref).reshape(2, 3, 5, 20).permute(0, 1, 3, 2).numpy()
+    assert np.allclose(y, ref, rtol=1e-12, atol=1e-13)
+    assert np.array_equal(sT, x[:, :, -3:])
+
+
+def test_conv_definition_resumes_from_its_state():
+    r = np.random.default_rng(1)
+    x, w = r.standard_normal((1, 2, 11, 3)), r.standard_normal((2, 3, 3))
+    y, sT = O.short_conv(x, w)
+    y1, s1 = O.short_conv(x[:, :, :1], w)
+    y2, s2 = O.short_conv(x[:, :, 1:], w, s0=s1)
+    assert np.array_equal(np.concatenate([y1, y2], 2), y) and np.array_equal(s2, sT)
+
+
+def test_scan_definition_closed_forms():
+    """Constant inputs: a geometric series; A = 0: a sum; lengths stop the state."""
+    T, dt = 30, 0.25
+    one = np.ones((1, T, 1))
+    B = np.ones((1, T, 1, 8))
+    A = -np.arange(1.0, 9.0)[None]
+    y, h = O.selective_scan(one, dt * one, A, B, B, use_softplus=False)
+    a = np.exp(dt * A[0])
+    assert np.allclose(h[0, 0], dt * (1 - a ** T) / (1 - a), rtol=1e-12)
+    assert np.allclose(y[0, -1, 0], h.sum(), rtol=1e-12)
+    _, h = O.selective_scan(one, dt * one, 0 * A, B, B, use_softplus=False, lens=[7])
+    assert np.allclose(h, 7 * dt, rtol=1e-14)
+    y, _ = O.selective_scan(one, dt * one, A, B, 0 * B, D=np.full(1, 3.0), z=2 * one,
+                            use_softplus=False)
+    assert np.allclose(y, 3 * 2 / (1 + np.exp(-2)), rtol=1e-14)
+
+
+def test_scan_definition_is_linear_attention_when_the_decay_is_shared():
+    """exp(dt A) the same for every entry: the state is a decayed sum of
+    (dt u) B^T, read by C: the linear rule with a scalar decay."""
+    import oracle
+    r = np.random.default_rng(5)
+    T, D, N = 25, 6, 8
+    u, B, C = r.standard_normal((1, T, D)), r.standard_normal((1, T, 1, N)), r.standard_normal((1, T, 1, N))
+    dt = np.repeat(r.uniform(0.05, 0.5, (1, T, 1)), D, axis=2)
+    y, h = O.selective_scan(u, dt, -np.ones((D, N)), B, C, use_softplus=False)
+    # a_t = exp(-exp(log_alpha)) = exp(-dt)
+    o, S = oracle.linear(C[0, :, 0], B[0, :, 0], (dt * u)[0], np.log(dt[0, :, 0]))
+    # oracle.linear takes its inputs rounded to float32.  Three factors of a term are off by
+    # 2^-24 each; log_alpha, at most 3 in size, by 3 2^-24, which moves log a = -dt by
+    # dt 3 2^-24 <= 1.5 2^-24 in each of at most T steps: relative to the sums of absolute
+    # terms, (3 + 1.5 T) 2^-24
+    ym, hm = O.selective_scan(abs(u), dt, -np.ones((D, N)), abs(B), abs(C), use_softplus=False)
+    tol = (3 + 1.5 * T) * 2.0 ** -24
+    assert (np.abs(y[0] - o) <= tol * ym[0]).all()
+    assert (np.abs(h[0] - S.T) <= tol * hm[0]).all()
+
+
+def _conv(lib, **kw):
+    a = dict(x=FAKE, sb=0, sh=0, st=0, w=FAKE, bias=None, s0=None, lens=None, y=FAKE, sT=FAKE, B=1,
+             H=1, T=4, d=8, W=4, dt=0, act=1, stream=None)
+    a.update(kw)
+    return lib.kda_short_conv(*a.values())
+
+
+def test_conv_refuses_before_any_launch(lib):
+    assert _conv(lib, dt=2) == INV and _conv(lib, act=2) == INV
+    assert _conv(lib, B=-1) == INV and _conv(lib, d=0) == INV and _conv(lib, T=-1) == INV
+    assert _conv(lib, st=-1) == INV and _conv(lib, sb=-8) == INV
+    assert _conv(lib, W=5) == UNS and _conv(lib, W=1) == UNS
+    assert _conv(lib, x=None) == INV and _conv(lib, w=None) == INV and _conv(lib, y=None) == INV
+    assert _conv(lib, x=FAKE + 2) == INV               # not a float32 address
+    assert _conv(lib, x=FAKE + 1, dt=1) == INV
+    for k in ("w", "bias", "s0", "y", "sT"):
+        assert _conv(lib, **{k: FAKE + 4}) == INV, k
+    assert _conv(lib, lens=FAKE + 2) == INV
+    assert _conv(lib, B=0) == OK and _conv(lib, T=0, sT=None) == OK  # nothing to do
+
+
+def test_conv_step_refuses_before_any_launch(lib):
+    def call(**kw):
+        a = dict(x=FAKE, sn=0, sh=0, w=FAKE, bias=None, S=FAKE, slots=FAKE, P=4, y=FAKE, N=3, H=1,
+                 d=8, W=4, dt=0, act=1, stream=None)
+        a.update(kw)
+        return lib.kda_short_conv_step(*a.values())
+    assert call(dt=5) == INV and call(act=-1) == INV and call(N=-1) == INV and call(P=-1) == INV
+    assert call(slots=None, P=2) == INV and call(W=8) == UNS and call(sn=-1) == INV
+    for k in ("x", "w", "S", "y"):
+        assert call(**{k: None}) == INV, k
+    for k in ("w", "bias", "S", "y"):
+        assert call(**{k: FAKE + 8}) == INV, k
+    assert call(slots=FAKE + 1) == INV
+    assert call(N=0) == OK and call(P=0) == OK
+
+
+def test_scan_refuses_before_any_launch(lib):
+    def call(**kw):
+        a = dict(u=FAKE, delta=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, db=None, h0=None,
+                 lens=None, y=FAKE, hT=FAKE, st=[0] * 10, B=1, T=4, Dn=8, G=2, N=16, dt=0, flags=1,
+                 ws=FAKE, wsb=1 << 30, stream=None)
+        a.update(kw)
+        a["st"] = None if a["st"] is None else (ctypes.c_longlong * 10)(*a["st"])
+        return lib.kda_selective_scan(*a.values())
+    assert call(dt=2) == INV and call(flags=2) == INV and call(B=-1) == INV and call(T=-1) == INV
+    assert call(Dn=0) == INV and call(G=0) == INV and call(G=3) == INV
+    assert call(N=12) == UNS and call(N=128) == UNS
+    for k in ("u", "delta", "A", "Bm", "Cm", "y", "st", "ws"):
+        assert call(**{k: None}) == INV, k
+    for k in ("A", "D", "db", "h0", "y", "hT"):
+        assert call(**{k: FAKE + 4}) == INV, k
+    for k in ("u", "delta", "Bm", "Cm", "z", "lens"):
+        assert call(**{k: FAKE + 2}) == INV, k
+    for i in range(10):
+        st = [0] * 10
+        st[i] = -1
+        assert call(st=st, z=FAKE) == INV, i
+    assert call(ws=FAKE + 16) == INV and call(wsb=16) == INV
+    assert call(B=0) == OK and call(T=0, hT=None) == OK
+    ws = lib.kda_selective_scan_workspace_size
+    assert ws(1, 4, 8, 2, 16, 0) >= 256 and ws(1, 4, 8, 3, 16, 0) == 0 and ws(1, 4, 8, 1, 4, 0) == 0
+    assert ws(1, 0, 8, 1, 16, 1) >= 256 and ws(0, 4, 8, 1, 16, 1) >= 256
+
+
+def test_step_refuses_before_any_launch(lib):
+    def call(**kw):
+        a = dict(u=FAKE, delta=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, z=None, db=None, S=FAKE,
+                 slots=None, P=4, y=FAKE, st=[0] * 5, R=3, Dn=8, G=2, N=16, dt=1, flags=0,
+                 stream=None)
+        a.update(kw)
+        a["st"] = None if a["st"] is None else (ctypes.c_longlong * 5)(*a["st"])
+        return lib.kda_selective_step(*a.values())
+    assert call(dt=-1) == INV and call(flags=4) == INV and call(R=-1) == INV and call(P=-1) == INV
+    assert call(P=2) == INV and call(G=3) == INV and call(N=24) == UNS
+    for k in ("u", "delta", "A", "Bm", "Cm", "S", "y", "st"):
+        assert call(**{k: None}) == INV, k
+    for k in ("A", "D", "db", "S", "y"):
+        assert call(**{k: FAKE + 8}) == INV, k
+    assert call(u=FAKE + 1) == INV and call(st=[0, 0, -1, 0, 0]) == INV
+    assert call(R=0) == OK
+
+
+def test_state_copy_and_clear_refuse_before_any_launch(lib):
+    def ix(*v):
+        return (ctypes.c_int * len(v))(*v)
+
+    def copy(pool=FAKE, L=1, ls=0, P=4, nb=16, src=ix(0), dst=ix(1), n=1):
+        return lib.kda_state_copy(pool, L, ls, P, nb, src, dst, n, None)
+    for bad in (dict(L=-1), dict(P=-1), dict(nb=-1), dict(n=-1), dict(ls=-1), dict(L=2, ls=63),
+                dict(src=ix(4)), dict(src=ix(-1)), dict(dst=ix(4)), dict(src=None), dict(dst=None),
+                dict(pool=None), dict(nb=1 << 62), dict(src=ix(0, 9), dst=ix(1, 2), n=2)):
+        assert copy(**bad) == INV, bad
+    assert copy(n=0) == OK and copy(L=0) == OK and copy(nb=0) == OK and copy(dst=ix(0)) == OK
+
+    def clear(pool=FAKE, L=1, ls=0, P=4, nb=16, s=ix(0), n=1):
+        return lib.kda_state_clear(pool, L, ls, P, nb, s, n, None)
+    for bad in (dict(s=ix(4)), dict(s=None), dict(pool=None), dict(nb=-1), dict(L=2, ls=1)):
+        assert clear(**bad) == INV, bad
+    assert clear(n=0) == OK and clear(nb=0) == OK
+
+
+def test_binding_refuses_host_tensors(lib):
+    import gated_delta_rule_wise_gb300 as kda
+    x, w = torch.zeros((1, 1, 4, 8)), torch.zeros((1, 8, 4))
+    for f in (lambda: kda.short_conv(x, w), lambda: kda.short_conv_step(x[:, :, 0], w, x[:, :, :3]),
+              lambda: kda.state_copy(torch.zeros((4, 8)), [0], [1]),
+              lambda: kda.state_clear(torch.zeros((4, 8)), [0])):
+        with pytest.raises(ValueError):
+            f()
