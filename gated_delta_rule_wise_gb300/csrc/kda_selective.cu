@@ -9,6 +9,8 @@
 // state it decays is off by a like amount whatever the sequence's length.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "kda_launch.cuh"
 
 namespace kda {
@@ -21,7 +23,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
-__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 struct Rows {  // a strided input: batch and token stride in elements
   const void *p;
@@ -37,55 +39,499 @@ struct ScanArgs {
   int B, T, D, G, softplus;
 };
 
-// One group of N / 4 lanes per (batch row, channel), token after token.
-template <typename TI, int N>
-__global__ void __launch_bounds__(kScanThreads) selective_scan_kernel(ScanArgs a) {
-  constexpr int L = N / kPer;
-  const long long id = (long long)blockIdx.x * (kScanThreads / L) + threadIdx.x / L;
-  const int lane = threadIdx.x % L;
-  const bool live = id < (long long)a.B * a.D;
-  const int b = live ? (int)(id / a.D) : 0, c = live ? (int)(id % a.D) : 0;
-  const int g = c / (a.D / a.G);
+// ---------------------------------------------------------------- prompts
+
+// Two float32 values in one 64-bit register pair: the packed products and sums
+// below issue once for both.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr int kMaxSplit = 64;      // parts of a sequence
+constexpr int kTargetWarps = 1216; // 152 SMs x 4 schedulers x 2
+constexpr unsigned kVecU = 1, kVecDelta = 2, kVecB = 4, kVecC = 8, kVecZ = 16;
+
+struct ScanPlan {
+  float *state;  // [split][B][D][N]: 0: h0; j: what part j - 1 leaves (0 from h0, others from 0)
+  float *sum;    // [split][B][D]: sum of part j's step sizes
+  int split, part;  // parts of a sequence, tokens of one
+  int tiles_g;      // channel tiles of a group
+  unsigned vec;     // inputs that can be read two (u, delta, z) or four (B, C) values at a time
+  bool pairs;       // every row of y starts on two values
+};
+
+// ----- two stored values: as loaded, and as a packed float32 pair
+template <typename TI> struct Two;
+template <> struct Two<__nv_bfloat16> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ raw join(__nv_bfloat16 lo, __nv_bfloat16 hi) {
+    return (uint32_t)__bfloat16_as_ushort(lo) | (uint32_t)__bfloat16_as_ushort(hi) << 16;
+  }
+  static __device__ __forceinline__ f2 widen(raw v) {
+    return pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ void st(__nv_bfloat16 *p, f2 v) {
+    const float2 x = unpack(v);
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x.x, x.y);
+  }
+};
+template <> struct Two<float> {
+  typedef f2 raw;
+  static __device__ __forceinline__ raw join(float lo, float hi) { return pack(lo, hi); }
+  static __device__ __forceinline__ f2 widen(raw v) { return v; }
+  static __device__ __forceinline__ void st(float *p, f2 v) { *reinterpret_cast<f2 *>(p) = v; }
+};
+// n (0, 1, 2) values from p on; `wide`: both in one load.  What is missing is zero.
+template <typename TI>
+__device__ __forceinline__ typename Two<TI>::raw load_two(const TI *p, int n, bool wide) {
+  if (wide) return n > 0 ? *reinterpret_cast<const typename Two<TI>::raw *>(p) : 0;
+  return Two<TI>::join(n > 0 ? p[0] : TI(0.f), n > 1 ? p[1] : TI(0.f));
+}
+__device__ __forceinline__ f2 both(float x) { return pack(x, x); }
+
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  The argument's
+// rounding is put back into e (its residual is exact in one fma).  log1p(e) / e
+// is a polynomial of degree 9, the least relative maximum error on [0, 1]
+// (4.7e-9, found by reweighted least squares on Chebyshev points); in float32
+// its values are within 2.6 2^-24 relative, so small steps keep their precision.
+__device__ __forceinline__ f2 softplus2(f2 x) {
+  const float2 v = unpack(x);
+  const f2 m = pack(-fabsf(v.x), -fabsf(v.y));
+  const f2 t = mul2(m, both(kLog2e));
+  const float2 tt = unpack(t);
+  const f2 r = fma2(m, both(kLog2e), pack(-tt.x, -tt.y));
+  const f2 e0 = pack(ex2(tt.x), ex2(tt.y));
+  const f2 e = fma2(mul2(e0, both(0.6931471805599453f)), r, e0);
+  f2 s = fma2(e, both(-3.244021209e-03f), both(1.985144429e-02f));
+  s = fma2(s, e, both(-5.695949867e-02f));
+  s = fma2(s, e, both(1.060365140e-01f));
+  s = fma2(s, e, both(-1.530559063e-01f));
+  s = fma2(s, e, both(1.967593879e-01f));
+  s = fma2(s, e, both(-2.495413423e-01f));
+  s = fma2(s, e, both(3.332996368e-01f));
+  s = fma2(s, e, both(-4.999990165e-01f));
+  s = fma2(s, e, both(1.f));
+  return fma2(s, e, pack(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
+// How a CTA is cut: REC recurrence threads, each with PER entries of CH channels;
+// IO threads that prepare operands and as many that write y.
+template <int CH_, int PER_, int REC_, int IO_> struct Cut {
+  static constexpr int CH = CH_, PER = PER_, REC = REC_, IO = IO_;
+};
+template <int N, class X, bool kOut> struct ScanShape {
+  static constexpr int L = N / X::PER;             // lanes that share a group of CH channels
+  static constexpr int CT = X::REC / L * X::CH;    // channels of a CTA
+  static constexpr int TT = CT >= 128 ? 8 : CT >= 64 ? 16 : 32;  // tokens of a tile
+  static constexpr int kThreads = X::REC + (kOut ? 2 : 1) * X::IO;
+  static constexpr int kDx = 2 * TT * CT * 8;  // (dt, dt u), two tiles
+  static constexpr int kBC = (kOut ? 4 : 2) * TT * N * 4;
+  static constexpr int kY = kOut ? 2 * TT * CT * 4 : 0;
+  static constexpr int kSmem = kDx + kBC + kY;
+};
+
+// Four values v[i] summed over the L lanes of a group, one exchange per step:
+// halves of the values change sides, then whole sums.  Lane i (of four) ends
+// with value i, two lanes with two values each, one lane with all.
+template <int L> struct LaneSums {
+  float v[4], keep[2], got[2];
+  __device__ __forceinline__ void step(int s, int lane) {
+    if (s == 0 && L == 2) {
+      send(lane & 1, 1);
+    } else if (s == 0 && L >= 4) {
+      send(lane & 2, 2);
+    } else if (s == 1 && L == 2) {
+      v[0] = keep[0] + got[0], v[1] = keep[1] + got[1];
+    } else if (s == 1 && L >= 4) {
+      const float a = keep[0] + got[0], b = keep[1] + got[1];
+      const bool odd = lane & 1;
+      keep[0] = odd ? b : a;
+      got[0] = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    } else if (s == 2 && L >= 4) {
+      v[0] = keep[0] + got[0];
+      if (L >= 8) got[0] = __shfl_xor_sync(0xffffffffu, v[0], 4);
+    } else if (s == 3 && L >= 8) {
+      v[0] += got[0];
+      if (L >= 16) got[0] = __shfl_xor_sync(0xffffffffu, v[0], 8);
+    } else if (s == 4 && L >= 16) {
+      v[0] += got[0];
+    }
+  }
+  __device__ __forceinline__ void send(bool hi, int off) {
+    keep[0] = hi ? v[2] : v[0], keep[1] = hi ? v[3] : v[1];
+    got[0] = __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], off);
+    got[1] = __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], off);
+  }
+};
+
+// Part blockIdx.y of a sequence: kOut writes y (and, in the last part, hT);
+// else only the state that the part leaves.
+template <typename TI, int N, class X, bool kOut>
+__global__ void __launch_bounds__(ScanShape<N, X, kOut>::kThreads, 2)
+selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
+  using S = ScanShape<N, X, kOut>;
+  constexpr int L = S::L, CT = S::CT, TT = S::TT;
+  constexpr int CH = X::CH, PER = X::PER, kRec = X::REC, kIo = X::IO;
+  extern __shared__ __align__(16) char smem[];
+  char *dx = smem;
+  char *bc = dx + S::kDx;
+  float *ys = reinterpret_cast<float *>(bc + S::kBC);
+
+  const int b = blockIdx.x / (a.G * p.tiles_g);
+  const int g = blockIdx.x / p.tiles_g % a.G;
+  const int per_g = a.D / a.G;
+  const int c_in_g = blockIdx.x % p.tiles_g * CT;
+  const int c0 = g * per_g + c_in_g;
+  const int chans = min(CT, per_g - c_in_g);
+  const int part = blockIdx.y;
   const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-  const TI *u = static_cast<const TI *>(a.u.p) + b * a.u.sb + c;
-  const TI *de = static_cast<const TI *>(a.delta.p) + b * a.delta.sb + c;
-  const TI *Bm = static_cast<const TI *>(a.Bm.p) + b * a.Bm.sb + (long long)g * N + lane * kPer;
-  const TI *Cm = static_cast<const TI *>(a.Cm.p) + b * a.Cm.sb + (long long)g * N + lane * kPer;
-  const TI *z = static_cast<const TI *>(a.z.p);
-  if (z) z += b * a.z.sb + c;
-  const long long so = ((long long)b * a.D + c) * N + lane * kPer;
-  const float bias = a.bias ? a.bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
-  float A2[kPer], h[kPer];
+  const int t0 = part * p.part;
+  const int t1 = min(len, t0 + p.part);
+  const bool last = t1 == len;  // the part that ends the sequence (the first one if it is empty)
+  if (part > 0 && t0 >= len) return;
+  if (!kOut && last && part > 0) return;  // nothing follows it
+  // (nothing follows a first part that ends the sequence: it only copies h0)
+  const int tiles = !kOut && last ? 0 : (t1 - t0 + TT - 1) / TT;
+
+  const int tid = threadIdx.x;
+  if (tid < kRec) {
+    // ---- recurrence: L lanes of PER entries share CH channels
+    const int ch = tid / L * CH, lane = tid % L, n0 = lane * PER;
+    const long long plane = (long long)a.B * a.D * N;
+    f2 A2[CH][PER / 2], h[CH][PER / 2];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    A2[k] = a.A[(long long)c * N + lane * kPer + k] * kLog2e;
-    h[k] = a.h0 ? a.h0[so + k] : 0.f;
-  }
-  // the lanes of a group share b, hence the trip count; a warp's groups may not
-  for (int t = 0; t < len; ++t) {
-    const float ut = Io<TI>::ld(u + t * a.u.st);
-    float dt = Io<TI>::ld(de + t * a.delta.st) + bias;
-    if (a.softplus) dt = softplus(dt);
-    const float x = dt * ut;
-    float acc = 0.f;
+    for (int j = 0; j < CH; ++j) {
+      const bool live = ch + j < chans;
+      const int c = c0 + (live ? ch + j : 0);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      h[k] = exp2f(dt * A2[k]) * h[k] + x * Io<TI>::ld(Bm + t * a.Bm.st + k);
-      acc += h[k] * Io<TI>::ld(Cm + t * a.Cm.st + k);
+      for (int i = 0; i < PER / 4; ++i) {
+        const long long so = ((long long)b * a.D + c) * N + n0 + 4 * i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), s = v;
+        if (live) v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + n0 + 4 * i);
+        v.x *= kLog2e, v.y *= kLog2e, v.z *= kLog2e, v.w *= kLog2e;
+        if (part == 0) {
+          // (a split sequence takes h0 from its copy: the last part may have written hT over it)
+          const float *from = kOut && p.split > 1 ? p.state : a.h0;
+          if (live && from) s = *reinterpret_cast<const float4 *>(from + so);
+          if (!kOut && live) *reinterpret_cast<float4 *>(p.state + so) = s;
+        } else if (kOut && live) {
+          // the state at the part's start, from what the parts before left
+          s = *reinterpret_cast<const float4 *>(p.state + plane + so);
+          for (int k = 1; k < part; ++k) {
+            const float sum = p.sum[((long long)k * a.B + b) * a.D + c];
+            const float4 e = *reinterpret_cast<const float4 *>(p.state + (k + 1) * plane + so);
+            s.x = fmaf(ex2(sum * v.x), s.x, e.x), s.y = fmaf(ex2(sum * v.y), s.y, e.y);
+            s.z = fmaf(ex2(sum * v.z), s.z, e.z), s.w = fmaf(ex2(sum * v.w), s.w, e.w);
+          }
+        }
+        A2[j][2 * i] = pack(v.x, v.y), A2[j][2 * i + 1] = pack(v.z, v.w);
+        h[j][2 * i] = pack(s.x, s.y), h[j][2 * i + 1] = pack(s.z, s.w);
+      }
     }
-    const unsigned mask = ((L == 32 ? 0u : (1u << (L & 31))) - 1u) << (threadIdx.x % 32 / L * L);
+    // Blocks of TB tokens give the four sums (token, channel) that lane_sums takes; the next
+    // block's operands are fetched before this one's sums are stored, which loads may not pass.
+    constexpr int TB = 4 / CH;
+    struct Block {
+      float2 d[TB][CH];
+      ulonglong2 B[TB][PER / 4], C[TB][PER / 4];
+    };
+    float sum[CH] = {};
+    __syncthreads();
+    for (int k = 0; k < tiles; ++k) {
+      const char *q = dx + ((k & 1) * TT * CT + ch) * 8;
+      const char *Bk = bc + ((k & 1) * TT * N + n0) * 4;
+      // value i of a block: token i / CH, channel i % CH; a lane stores kOwn of them
+      constexpr int kOwn = L >= 4 ? 1 : 4 / L;
+      float *yk = ys + (k & 1) * TT * CT + ch + lane % 4 * kOwn / CH * CT + lane % 4 * kOwn % CH;
+      const auto fetch = [&](Block &x, int t) {
 #pragma unroll
-    for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(mask, acc, off);
-    if (live && lane == 0) {
-      acc += skip * ut;
-      if (z) acc *= silu(Io<TI>::ld(z + t * a.z.st));
-      Io<TI>::st(static_cast<TI *>(a.y) + ((long long)b * a.T + t) * a.D + c, acc);
+        for (int i = 0; i < TB; ++i) {
+          if (CH == 1) {
+            x.d[i][0] = *reinterpret_cast<const float2 *>(q + (t + i) * CT * 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+              const float4 v = *reinterpret_cast<const float4 *>(q + (t + i) * CT * 8 + j * 8);
+              x.d[i][j] = make_float2(v.x, v.y);
+              x.d[i][j + 1] = make_float2(v.z, v.w);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < PER / 4; ++j) {
+            x.B[i][j] = *reinterpret_cast<const ulonglong2 *>(Bk + (t + i) * N * 4 + j * 16);
+            if (kOut)
+              x.C[i][j] = *reinterpret_cast<const ulonglong2 *>(Bk + (2 * TT + t + i) * N * 4 + j * 16);
+          }
+        }
+      };
+      float tile_sum[CH] = {};
+      // The sums over lanes of the block before run between this one's products:
+      // each exchange has a quarter of a block to come back.
+      LaneSums<L> sums{};
+      const auto store = [&](int t) {
+        if (L <= 4 || lane < 4) {
+#pragma unroll
+          for (int i = 0; i < kOwn; ++i) yk[(t + i / CH) * CT + i % CH] = sums.v[i];
+        }
+      };
+      const auto work = [&](const Block &x, int t) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) {
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            if (kOut) sums.step(i * CH + j, lane);
+            const f2 dt = both(x.d[i][j].x), xu = both(x.d[i][j].y);
+            f2 s;
+#pragma unroll
+            for (int n = 0; n < PER / 2; ++n) {
+              const ulonglong2 Bn = x.B[i][n / 2], Cn = x.C[i][n / 2];
+              const float2 e = unpack(mul2(A2[j][n], dt));
+              h[j][n] = fma2(pack(ex2(e.x), ex2(e.y)), h[j][n], mul2(xu, n % 2 ? Bn.y : Bn.x));
+              if (kOut) {
+                const f2 c = n % 2 ? Cn.y : Cn.x;
+                s = n ? fma2(h[j][n], c, s) : mul2(h[j][n], c);
+              }
+            }
+            if (kOut) {
+              const float2 w = unpack(s);
+              y[i * CH + j] = w.x + w.y;
+            } else {
+              tile_sum[j] += x.d[i][j].x;
+            }
+          }
+        }
+        if (kOut) {
+          sums.step(4, lane);
+          if (t > 0) store(t - TB);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sums.v[i] = y[i];
+        }
+      };
+      Block x0, x1;
+      fetch(x0, 0);
+#pragma unroll 1
+      for (int t = 0; t < TT; t += 2 * TB) {
+        fetch(x1, t + TB);
+        work(x0, t);
+        fetch(x0, t + 2 * TB < TT ? t + 2 * TB : 0);
+        work(x1, t + TB);
+      }
+      if (kOut) {
+#pragma unroll
+        for (int s = 0; s <= 4; ++s) sums.step(s, lane);
+        store(TT - TB);
+      }
+#pragma unroll
+      for (int j = 0; j < CH; ++j) sum[j] += tile_sum[j];
+      __syncthreads();
     }
-  }
-  if (live && a.hT) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) a.hT[so + k] = h[k];
+    for (int j = 0; j < CH; ++j) {
+      if (ch + j >= chans) continue;
+      const int c = c0 + ch + j;
+      const long long so = ((long long)b * a.D + c) * N + n0;
+      float *to = kOut ? (last ? a.hT : nullptr) : p.state + (part + 1) * plane;
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i) {
+        const float2 s0 = unpack(h[j][2 * i]), s1 = unpack(h[j][2 * i + 1]);
+        if (to) *reinterpret_cast<float4 *>(to + so + 4 * i) = make_float4(s0.x, s0.y, s1.x, s1.y);
+      }
+      if (!kOut && n0 == 0) p.sum[((long long)part * a.B + b) * a.D + c] = sum[j];
+    }
+    return;
   }
+
+  // This thread's two channels, its first token of a tile and the step to its next.
+  constexpr int kRows = kIo / (CT / 2), kTimes = (TT + kRows - 1) / kRows;
+  const int io = (tid - kRec) % kIo;
+  const int ch = io % (CT / 2) * 2, tr = io / (CT / 2);
+  const int two = min(max(chans - ch, 0), 2);
+  const auto per_channel = [&](const float *q) {
+    return q ? pack(two > 0 ? q[c0 + ch] : 0.f, two > 1 ? q[c0 + ch + 1] : 0.f) : 0;
+  };
+  typedef typename Two<TI>::raw raw2;
+  // Two channels of the thread's tokens; q is the first one's place in the tile.
+  const auto rows_of = [&](raw2 (&v)[kTimes], const TI *q, long long step, int rows, bool wide) {
+    if (wide && rows >= TT && two == 2 && kRows * kTimes == TT) {
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) v[i] = *reinterpret_cast<const raw2 *>(q + i * step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) {
+        const int t = tr + i * kRows;
+        v[i] = load_two<TI>(q + i * step, t < rows && t < TT ? two : 0, wide);
+      }
+    }
+  };
+  const auto place = [&](const Rows &x) {
+    return static_cast<const TI *>(x.p) + b * x.sb + c0 + ch + (t0 + tr) * x.st;
+  };
+  const TI *u = place(a.u);
+  const long long u_step = kRows * a.u.st, u_tile = TT * a.u.st;
+
+  if (tid < kRec + kIo) {
+    // ---- step sizes, B and C of the next tile, read one tile further ahead
+    const TI *de = place(a.delta);
+    const long long d_step = kRows * a.delta.st, d_tile = TT * a.delta.st;
+    // four values of B and C: token io / (N / 4) of a tile, and kIo / (N / 4) tokens on
+    const int qt = io / (N / 4);
+    const auto group = [&](const Rows &x) {
+      return static_cast<const TI *>(x.p) + b * x.sb + (long long)g * N + io % (N / 4) * 4 +
+             (t0 + qt) * x.st;
+    };
+    const TI *Bm = group(a.Bm), *Cm = group(a.Cm);
+    constexpr int kQuads = TT * N / 4 / kIo;  // groups of four values of B, and of C
+    static_assert(kQuads * kIo * 4 == TT * N || TT * N / 4 < kIo, "whole rounds");
+    constexpr int kQ = kQuads > 0 ? kQuads : 1;
+    const bool has_quad = TT * N / 4 >= kIo || io < TT * N / 4;
+    raw2 ru[kTimes], rd[kTimes], rB[kQ][2], rC[kQ][2];
+    const f2 bias = per_channel(a.bias);
+    const auto quad = [&](raw2 (&v)[2], const TI *q, int t, int rows, bool wide) {
+      const bool in = has_quad && t < rows;
+      if (wide) {
+        typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
+        four w{};
+        if (in) w = *reinterpret_cast<const four *>(q);
+        v[0] = w.x, v[1] = w.y;
+      } else {
+        v[0] = load_two<TI>(q, in ? 2 : 0, false), v[1] = load_two<TI>(q + 2, in ? 2 : 0, false);
+      }
+    };
+    int ahead = t1 - t0;  // tokens from the tile that is read next to the end
+    const auto load = [&]() {
+      rows_of(ru, u, u_step, ahead, p.vec & kVecU);
+      rows_of(rd, de, d_step, ahead, p.vec & kVecDelta);
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        constexpr int kStep = kIo / (N / 4);
+        quad(rB[i], Bm + i * kStep * a.Bm.st, qt + i * kStep, ahead, p.vec & kVecB);
+        if (kOut) quad(rC[i], Cm + i * kStep * a.Cm.st, qt + i * kStep, ahead, p.vec & kVecC);
+      }
+      u += u_tile, de += d_tile, Bm += TT * a.Bm.st, Cm += TT * a.Cm.st, ahead -= TT;
+    };
+    // A token behind the end gets step 0 and B = 0: decay 1, nothing added.
+    const auto prepare = [&](int k) {
+      char *q = dx + ((k & 1) * TT * CT + ch) * 8;
+      const int rows = t1 - t0 - k * TT;
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) {
+        const int t = tr + i * kRows;
+        f2 dt = add2(Two<TI>::widen(rd[i]), bias);
+        if (a.softplus) dt = softplus2(dt);
+        if (t >= rows) dt = 0;
+        const float2 d = unpack(dt), v = unpack(mul2(dt, Two<TI>::widen(ru[i])));
+        if (kRows * kTimes == TT || t < TT)
+          *reinterpret_cast<float4 *>(q + t * CT * 8) = make_float4(d.x, v.x, d.y, v.y);
+      }
+      float *fb = reinterpret_cast<float *>(bc) + (k & 1) * TT * N;
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        if (!has_quad) continue;
+        const int e = (io + i * kIo) * 4;
+        *reinterpret_cast<ulonglong2 *>(fb + e) =
+            ulonglong2{Two<TI>::widen(rB[i][0]), Two<TI>::widen(rB[i][1])};
+        if (kOut)
+          *reinterpret_cast<ulonglong2 *>(fb + 2 * TT * N + e) =
+              ulonglong2{Two<TI>::widen(rC[i][0]), Two<TI>::widen(rC[i][1])};
+      }
+    };
+    if (tiles > 0) {
+      load();
+      prepare(0);
+      load();
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+      if (k + 1 < tiles) {
+        prepare(k + 1);
+        load();
+      }
+      __syncthreads();
+    }
+    return;
+  }
+
+  // ---- y of the tile before: D u, the gate, rounding
+  const bool gated = a.z.p != nullptr;
+  const TI *z = place(a.z);
+  const long long z_step = kRows * a.z.st, z_tile = TT * a.z.st;
+  const f2 skip = per_channel(a.Dskip);
+  TI *y = static_cast<TI *>(a.y) + ((long long)b * a.T + t0 + tr) * a.D + c0 + ch;
+  const long long y_step = (long long)kRows * a.D, y_tile = (long long)TT * a.D;
+  raw2 ru[kTimes], rz[kTimes];
+  int rows = t1 - t0;  // tokens from the tile in work to the end
+  const auto load = [&](int left) {
+    rows_of(ru, u, u_step, left, p.vec & kVecU);
+    if (gated) rows_of(rz, z, z_step, left, p.vec & kVecZ);
+    u += u_tile, z += z_tile;
+  };
+  const auto write = [&](int k) {
+    const float *sy = ys + (k & 1) * TT * CT + tr * CT + ch;
+    f2 v[kTimes];
+#pragma unroll
+    for (int i = 0; i < kTimes; ++i) {
+      if (kRows * kTimes != TT && tr >= TT) break;
+      v[i] = fma2(skip, Two<TI>::widen(ru[i]), *reinterpret_cast<const f2 *>(sy + i * kRows * CT));
+      if (gated) {
+        const float2 gate = unpack(Two<TI>::widen(rz[i]));
+        v[i] = mul2(v[i], pack(silu(gate.x), silu(gate.y)));
+      }
+    }
+    if (p.pairs && rows >= TT && two == 2 && kRows * kTimes == TT) {
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) Two<TI>::st(y + i * y_step, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTimes; ++i) {
+        const int t = tr + i * kRows;
+        if (t >= rows || t >= TT) break;
+        const float2 w = unpack(v[i]);
+        if (two > 0) Io<TI>::st(y + i * y_step, w.x);
+        if (two > 1) Io<TI>::st(y + i * y_step + 1, w.y);
+      }
+    }
+    y += y_tile, rows -= TT;
+  };
+  if (tiles > 0) load(rows);
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < tiles; ++k) {
+    if (k > 0) {
+      write(k - 1);
+      load(rows);
+    }
+    __syncthreads();
+  }
+  if (tiles > 0) write(tiles - 1);
 }
 
 struct StepArgs {
@@ -133,13 +579,51 @@ __global__ void __launch_bounds__(kScanThreads) selective_step_kernel(StepArgs a
   }
 }
 
-template <typename TI, int N>
-kda_status launch_scan(const ScanArgs &a, cudaStream_t st) {
-  const long long per = kScanThreads / (N / kPer);
-  const long long blocks = ((long long)a.B * a.D + per - 1) / per;
+struct ScanChoice {
+  int cut, split;
+};
+// Two channels per lane group halve the reads of B and C per entry, and the warps: worth it
+// once the state alone fills the schedulers (8192 channels of 16 entries: 129 against 133 us
+// for 2048 tokens; 4096 channels: 990 against 590 us for 16384).  Where one channel per group
+// leaves most of them empty, the tokens are split as well, at the price of the exponentials
+// of a second pass: 1536 channels, 8192 tokens: 6 parts 146 us, one 305 us; 4096 channels:
+// 4 parts 746 us, one 590 us, so two parts never pay.
+ScanChoice scan_choice(int B, int T, int D, int N) {
+  const long long warps = ((long long)B * D * N + 127) / 128;  // with four entries per thread
+  ScanChoice c;
+  c.cut = warps >= kTargetWarps * 4 / 5 ? 2 : 1;
+  long long s = warps > 0 ? kTargetWarps / warps : 1;
+  if (s > T / 64) s = T / 64;
+  if (s > kMaxSplit) s = kMaxSplit;
+  c.split = s < 3 ? 1 : (int)s;
+  return c;
+}
+
+template <typename TI, int N, class X>
+kda_status launch_scan_cut(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
+  using So = ScanShape<N, X, true>;
+  using Ss = ScanShape<N, X, false>;
+  p.tiles_g = (a.D / a.G + So::CT - 1) / So::CT;
+  const long long blocks = (long long)a.B * a.G * p.tiles_g;
   if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  selective_scan_kernel<TI, N><<<(unsigned)blocks, kScanThreads, 0, st>>>(a);
+  if (cudaFuncSetAttribute(selective_scan_kernel<TI, N, X, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, So::kSmem) != cudaSuccess)
+    return KDA_ERR_CUDA;
+  if (p.split > 1) {
+    if (cudaFuncSetAttribute(selective_scan_kernel<TI, N, X, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Ss::kSmem) != cudaSuccess)
+      return KDA_ERR_CUDA;
+    selective_scan_kernel<TI, N, X, false>
+        <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
+  }
+  selective_scan_kernel<TI, N, X, true>
+      <<<dim3((unsigned)blocks, p.split), So::kThreads, So::kSmem, st>>>(a, p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+template <typename TI, int N>
+kda_status launch_scan(const ScanArgs &a, const ScanPlan &p, int cut, cudaStream_t st) {
+  if (cut == 2) return launch_scan_cut<TI, N, Cut<2, 4, 128, 128>>(a, p, st);
+  return launch_scan_cut<TI, N, Cut<1, 4, 128, 128>>(a, p, st);
 }
 template <typename TI, int N>
 kda_status launch_step(const StepArgs &a, cudaStream_t st) {
@@ -151,12 +635,12 @@ kda_status launch_step(const StepArgs &a, cudaStream_t st) {
 }
 
 template <typename TI>
-kda_status launch_scan_n(const ScanArgs &a, int N, cudaStream_t st) {
+kda_status launch_scan_n(const ScanArgs &a, const ScanPlan &p, int cut, int N, cudaStream_t st) {
   switch (N) {
-    case 8: return launch_scan<TI, 8>(a, st);
-    case 16: return launch_scan<TI, 16>(a, st);
-    case 32: return launch_scan<TI, 32>(a, st);
-    default: return launch_scan<TI, 64>(a, st);
+    case 8: return launch_scan<TI, 8>(a, p, cut, st);
+    case 16: return launch_scan<TI, 16>(a, p, cut, st);
+    case 32: return launch_scan<TI, 32>(a, p, cut, st);
+    default: return launch_scan<TI, 64>(a, p, cut, st);
   }
 }
 template <typename TI>
@@ -178,6 +662,7 @@ kda_status check_sizes(int B, int T, int D, int G, int N, kda_dtype dt, unsigned
   if ((flags & ~KDA_SCAN_SOFTPLUS) != 0u) return KDA_ERR_INVALID_ARG;
   if (B < 0 || T < 0 || D < 1 || G < 1 || D % G != 0) return KDA_ERR_INVALID_ARG;
   if (N != 8 && N != 16 && N != 32 && N != 64) return KDA_ERR_UNSUPPORTED;
+  if (T > (1 << 30)) return KDA_ERR_UNSUPPORTED;  // token counters stay in 32 bits
   return KDA_OK;
 }
 
@@ -186,7 +671,11 @@ kda_status check_sizes(int B, int T, int D, int G, int N, kda_dtype dt, unsigned
 
 extern "C" size_t kda_selective_scan_workspace_size(int B, int T, int D, int G, int N,
                                                     kda_dtype dt) {
-  return kda::check_sizes(B, T, D, G, N, dt, 0u) == KDA_OK ? 256 : 0;
+  using namespace kda;
+  if (check_sizes(B, T, D, G, N, dt, 0u) != KDA_OK) return 0;
+  if (B == 0) return 256;
+  const size_t split = (size_t)scan_choice(B, T, D, N).split;
+  return 256 + (split > 1 ? split * B * D * (N + 1) * sizeof(float) : 0);
 }
 
 extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const float *A,
@@ -218,8 +707,28 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
                    {z, z ? strides[8] : 0, z ? strides[9] : 0},
                    A, Dskip, delta_bias, h0, lens, y, hT, B, T, D, G,
                    (flags & KDA_SCAN_SOFTPLUS) != 0u};
+  ScanPlan p;
+  const ScanChoice choice = scan_choice(B, T, D, N);
+  p.split = choice.split;
+  // a part is whole tiles, so its tokens need no masks but at the sequence's end
+  p.part = (T + p.split * 32 - 1) / (p.split * 32) * 32;
+  p.pairs = D % 2 == 0 && D / G % 2 == 0;
+  p.tiles_g = 0;  // by the kernel's shape
+  p.state = static_cast<float *>(workspace);
+  p.sum = p.state + (size_t)p.split * B * D * N;
+  // wide reads: the address and both strides are multiples of n values, and
+  // no row of a group ends inside a pair
+  const auto wide = [&](const void *q, int i, int n) {
+    return (reinterpret_cast<uintptr_t>(q) | (uintptr_t)(strides[i] * e) |
+            (uintptr_t)(strides[i + 1] * e)) % (n * e) == 0;
+  };
+  p.vec = (wide(Bm, 4, 4) ? kVecB : 0) | (wide(Cm, 6, 4) ? kVecC : 0);
+  if (D / G % 2 == 0)
+    p.vec |= (wide(u, 0, 2) ? kVecU : 0) | (wide(delta, 2, 2) ? kVecDelta : 0) |
+             (z && wide(z, 8, 2) ? kVecZ : 0);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, N, st) : launch_scan_n<float>(a, N, st);
+  return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.cut, N, st)
+                        : launch_scan_n<float>(a, p, choice.cut, N, st);
 }
 
 extern "C" kda_status kda_selective_step(const void *u, const void *delta, const float *A,

@@ -436,8 +436,8 @@ kda_status kda_short_conv_step(const void *x, long long x_sn, long long x_sh, co
  *   strides     10 element strides in HOST memory, each >= 0: batch and token
  *               stride of u, delta, Bm, Cm and z in this order (those of z are
  *               not read when z is NULL)
- *   N in {8, 16, 32, 64}, G >= 1 divides D; else KDA_ERR_UNSUPPORTED /
- *   KDA_ERR_INVALID_ARG.
+ *   N in {8, 16, 32, 64} and T <= 2^30, else KDA_ERR_UNSUPPORTED; G >= 1
+ *   divides D.
  *   workspace   >= kda_selective_scan_workspace_size(...) bytes of device
  *               memory, 256-byte aligned, not shared with a concurrent call;
  *               it needs no initialisation.
