@@ -379,62 +379,67 @@ def decode_step(q, k, v, beta, log_alpha, S, stream=None):
 
 KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
 KDA_SCAN_SOFTPLUS = 1
+_Strides10, _Strides5 = _LL * 10, _LL * 5
 
 
-def _call(dev, stream, fn, what, *args):
-    """Call ``fn(*args, stream)`` with ``dev`` (the tensors' device) current."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), what)
+def _call(dev, stream, name, *args):
+    """Call the C function ``name`` with ``dev`` (the tensors' device index)
+    current, on ``stream`` or the device's current stream."""
+    fn = getattr(_lib or load_library(), name)
+    if dev == torch.cuda.current_device():
+        st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        status = fn(*args, st)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), what)
+            status = fn(*args, _stream(stream))
+    if status != KDA_OK:
+        raise KdaError(status, name)
 
 
 def _keep(stream, *tensors):
     """Tensors allocated here but used on a stream the caller chose: their
     memory is not handed out again before that stream has passed the call."""
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _refuse(t, name, shape, dtype, dev):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"libkda takes contiguous tensors: {name} has strides {t.stride()}")
 
 
 def _dense(t, name, shape, dtype, dev):
     """Pointer of a contiguous device tensor of this shape and type; None stays None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return _ptr(t)
-
-
-def _strided(t, name, shape, dtype, dev):
-    """Pointer of a device tensor of this shape and type whose last axis is dense."""
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.stride(-1) != 1 and shape[-1] > 1 and t.numel() > 0:
-        raise ValueError(f"the last axis of {name} must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, dev)
     return t.data_ptr()
 
 
+def _strided(t, name, shape, dtype, dev, dense=1):
+    """Pointer and strides of a device tensor of this shape and type whose last
+    ``dense`` axes are contiguous."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, shape, dtype, dev)
+    st = t.stride()
+    if (st[-1] != 1 and shape[-1] > 1 or
+            dense == 2 and st[-2] != shape[-1] and shape[-2] > 1) and t.numel() > 0:
+        raise ValueError(f"the last {dense} axes of {name} must be contiguous: strides {st}")
+    return t.data_ptr(), st
+
+
 def _device_of(t, name):
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"libkda takes device tensors: {name} is on {t.device}")
-    return t.device
-
-
-def _group_rows(t, name, shape, dtype, dev):
-    """Pointer of B or C, [..., G, N] with the last two axes dense."""
-    p = _strided(t, name, shape, dtype, dev)
-    if shape[-2] > 1 and t.stride(-2) != shape[-1] and t.numel() > 0:
-        raise ValueError(f"the last two axes of {name} must be contiguous")
-    return p
+    return dev
 
 
 def kda_short_conv(x, w, bias, s0, lens, y, sT, act=KDA_ACT_SILU, stream=None):
@@ -446,13 +451,13 @@ def kda_short_conv(x, w, bias, s0, lens, y, sT, act=KDA_ACT_SILU, stream=None):
     code = _dtype_code(x)
     B, H, T, d = x.shape
     W = w.shape[-1]
-    f32 = torch.float32
-    _call(dev, stream, load_library().kda_short_conv, "kda_short_conv",
-          _strided(x, "x", (B, H, T, d), dt, dev), x.stride(0), x.stride(1), x.stride(2),
-          _dense(w, "w", (H, d, W), f32, dev), _dense(bias, "bias", (H, d), f32, dev),
-          _dense(s0, "s0", (B, H, W - 1, d), dt, dev),
+    px, st = _strided(x, "x", (B, H, T, d), dt, dev)
+    state = (B, H, W - 1, d)
+    _call(dev, stream, "kda_short_conv", px, st[0], st[1], st[2],
+          _dense(w, "w", (H, d, W), torch.float32, dev),
+          _dense(bias, "bias", (H, d), torch.float32, dev), _dense(s0, "s0", state, dt, dev),
           _dense(lens, "lens", (B,), torch.int32, dev), _dense(y, "y", (B, H, T, d), dt, dev),
-          _dense(sT, "sT", (B, H, W - 1, d), dt, dev), B, H, T, d, W, code, act)
+          _dense(sT, "sT", state, dt, dev), B, H, T, d, W, code, act)
 
 
 def short_conv(x, w, bias=None, s0=None, lens=None, act=KDA_ACT_SILU, output_final_state=True,
@@ -461,11 +466,11 @@ def short_conv(x, w, bias=None, s0=None, lens=None, act=KDA_ACT_SILU, output_fin
     returns (y, sT or None).  With ``lens`` the rows of a new y behind a
     sequence's length hold nothing."""
     B, H, T, d = x.shape
-    y = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device) if out is None else out
-    sT = (torch.empty((B, H, w.shape[-1] - 1, d), dtype=x.dtype, device=x.device)
-          if output_final_state else None)
+    y = x.new_empty((B, H, T, d)) if out is None else out
+    sT = x.new_empty((B, H, w.shape[-1] - 1, d)) if output_final_state else None
     kda_short_conv(x, w, bias, s0, lens, y, sT, act, stream)
-    _keep(stream, y, sT)
+    if stream is not None:
+        _keep(stream, y, sT)
     return y, sT
 
 
@@ -477,10 +482,10 @@ def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
     code = _dtype_code(x)
     N, H, d = x.shape
     W, P = w.shape[-1], S.shape[0]
-    f32 = torch.float32
-    _call(dev, stream, load_library().kda_short_conv_step, "kda_short_conv_step",
-          _strided(x, "x", (N, H, d), dt, dev), x.stride(0), x.stride(1),
-          _dense(w, "w", (H, d, W), f32, dev), _dense(bias, "bias", (H, d), f32, dev),
+    px, st = _strided(x, "x", (N, H, d), dt, dev)
+    _call(dev, stream, "kda_short_conv_step", px, st[0], st[1],
+          _dense(w, "w", (H, d, W), torch.float32, dev),
+          _dense(bias, "bias", (H, d), torch.float32, dev),
           _dense(S, "S", (P, H, W - 1, d), dt, dev),
           _dense(slots, "slots", (N,), torch.int32, dev), P,
           _dense(y, "y", (N, H, d), dt, dev), N, H, d, W, code, act)
@@ -488,14 +493,15 @@ def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
 
 def short_conv_step(x, w, S, bias=None, slots=None, act=KDA_ACT_SILU, out=None, stream=None):
     """Allocate y (unless ``out`` is given) and run ``kda_short_conv_step``; returns y."""
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    y = x.new_empty(x.shape) if out is None else out
     kda_short_conv_step(x, w, bias, S, slots, y, act, stream)
-    _keep(stream, y)
+    if stream is not None:
+        _keep(stream, y)
     return y
 
 
 def kda_selective_scan_workspace_size(B, T, D, G, N, dtype) -> int:
-    return load_library().kda_selective_scan_workspace_size(B, T, D, G, N, dtype)
+    return (_lib or load_library()).kda_selective_scan_workspace_size(B, T, D, G, N, dtype)
 
 
 def selective_scan_workspace_for(u, A, B):
@@ -504,7 +510,7 @@ def selective_scan_workspace_for(u, A, B):
                                           A.shape[1], _dtype_code(u))
     if n == 0:
         raise KdaError(KDA_ERR_UNSUPPORTED, "kda_selective_scan_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=u.device)
+    return u.new_empty(n, dtype=torch.uint8)
 
 
 def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, workspace,
@@ -515,21 +521,20 @@ def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, wor
     y [B,T,D] (written; rows behind a sequence's length are left alone)."""
     dev, dt = _device_of(u, "u"), u.dtype
     code = _dtype_code(u)
-    nB, T, nD = u.shape
+    nB, T, nD = rows = u.shape
     G, N = B.shape[2], A.shape[1]
     f32 = torch.float32
-    st = (_LL * 10)(u.stride(0), u.stride(1), delta.stride(0), delta.stride(1), B.stride(0),
-                    B.stride(1), C.stride(0), C.stride(1),
-                    0 if z is None else z.stride(0), 0 if z is None else z.stride(1))
-    _call(dev, stream, load_library().kda_selective_scan, "kda_selective_scan",
-          _strided(u, "u", (nB, T, nD), dt, dev), _strided(delta, "delta", (nB, T, nD), dt, dev),
-          _dense(A, "A", (nD, N), f32, dev), _group_rows(B, "B", (nB, T, G, N), dt, dev),
-          _group_rows(C, "C", (nB, T, G, N), dt, dev), _dense(D, "D", (nD,), f32, dev),
-          None if z is None else _strided(z, "z", (nB, T, nD), dt, dev),
-          _dense(delta_bias, "delta_bias", (nD,), f32, dev),
+    pu, su = _strided(u, "u", rows, dt, dev)
+    pd, sd = _strided(delta, "delta", rows, dt, dev)
+    pB, sB = _strided(B, "B", (nB, T, G, N), dt, dev, 2)
+    pC, sC = _strided(C, "C", (nB, T, G, N), dt, dev, 2)
+    pz, sz = (None, (0, 0)) if z is None else _strided(z, "z", rows, dt, dev)
+    st = _Strides10(su[0], su[1], sd[0], sd[1], sB[0], sB[1], sC[0], sC[1], sz[0], sz[1])
+    _call(dev, stream, "kda_selective_scan", pu, pd, _dense(A, "A", (nD, N), f32, dev), pB, pC,
+          _dense(D, "D", (nD,), f32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), f32, dev),
           _dense(h0, "h0", (nB, nD, N), f32, dev), _dense(lens, "lens", (nB,), torch.int32, dev),
-          _dense(y, "y", (nB, T, nD), dt, dev), _dense(hT, "hT", (nB, nD, N), f32, dev),
-          st, nB, T, nD, G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
+          _dense(y, "y", rows, dt, dev), _dense(hT, "hT", (nB, nD, N), f32, dev), st, nB, T, nD,
+          G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
           workspace.numel() * workspace.element_size())
 
 
@@ -539,12 +544,12 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, 
     """Allocate y (unless ``out`` is given), hT and the workspace and run
     ``kda_selective_scan``; returns (y, hT or None).  With ``lens`` the rows of
     a new y behind a sequence's length hold nothing."""
-    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
-    hT = (torch.empty((u.shape[0],) + tuple(A.shape), dtype=torch.float32, device=u.device)
-          if output_final_state else None)
+    y = u.new_empty(u.shape) if out is None else out
+    hT = A.new_empty((u.shape[0],) + A.shape) if output_final_state else None
     ws = selective_scan_workspace_for(u, A, B) if workspace is None else workspace
     kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, ws, softplus, stream)
-    _keep(stream, y, hT, ws if workspace is None else None)
+    if stream is not None:
+        _keep(stream, y, hT, ws if workspace is None else None)
     return y, hT
 
 
@@ -555,28 +560,28 @@ def kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplu
     as in ``kda_short_conv_step``; y [R,D]."""
     dev, dt = _device_of(u, "u"), u.dtype
     code = _dtype_code(u)
-    R, nD = u.shape
+    R, nD = rows = u.shape
     G, N, P = B.shape[1], A.shape[1], S.shape[0]
     f32 = torch.float32
-    st = (_LL * 5)(u.stride(0), delta.stride(0), B.stride(0), C.stride(0),
-                   0 if z is None else z.stride(0))
-    _call(dev, stream, load_library().kda_selective_step, "kda_selective_step",
-          _strided(u, "u", (R, nD), dt, dev), _strided(delta, "delta", (R, nD), dt, dev),
-          _dense(A, "A", (nD, N), f32, dev), _group_rows(B, "B", (R, G, N), dt, dev),
-          _group_rows(C, "C", (R, G, N), dt, dev), _dense(D, "D", (nD,), f32, dev),
-          None if z is None else _strided(z, "z", (R, nD), dt, dev),
-          _dense(delta_bias, "delta_bias", (nD,), f32, dev),
+    pu, su = _strided(u, "u", rows, dt, dev)
+    pd, sd = _strided(delta, "delta", rows, dt, dev)
+    pB, sB = _strided(B, "B", (R, G, N), dt, dev, 2)
+    pC, sC = _strided(C, "C", (R, G, N), dt, dev, 2)
+    pz, sz = (None, (0,)) if z is None else _strided(z, "z", rows, dt, dev)
+    _call(dev, stream, "kda_selective_step", pu, pd, _dense(A, "A", (nD, N), f32, dev), pB, pC,
+          _dense(D, "D", (nD,), f32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), f32, dev),
           _dense(S, "S", (P, nD, N), f32, dev), _dense(slots, "slots", (R,), torch.int32, dev), P,
-          _dense(y, "y", (R, nD), dt, dev), st, R, nD, G, N, code,
-          KDA_SCAN_SOFTPLUS if softplus else 0)
+          _dense(y, "y", rows, dt, dev), _Strides5(su[0], sd[0], sB[0], sC[0], sz[0]), R, nD, G,
+          N, code, KDA_SCAN_SOFTPLUS if softplus else 0)
 
 
 def selective_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, slots=None,
                    softplus=True, out=None, stream=None):
     """Allocate y (unless ``out`` is given) and run ``kda_selective_step``; returns y."""
-    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
+    y = u.new_empty(u.shape) if out is None else out
     kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplus, stream)
-    _keep(stream, y)
+    if stream is not None:
+        _keep(stream, y)
     return y
 
 
@@ -619,7 +624,7 @@ def kda_state_copy(pool, src, dst, layered=False, stream=None):
     a, b = _index_list(src, "src"), _index_list(dst, "dst")
     if a.numel() != b.numel():
         raise ValueError("src and dst must have the same length")
-    _call(dev, stream, load_library().kda_state_copy, "kda_state_copy", *args, a.data_ptr(),
+    _call(dev, stream, "kda_state_copy", *args, a.data_ptr(),
           b.data_ptr(), a.numel())
 
 
@@ -627,7 +632,7 @@ def kda_state_clear(pool, slots, layered=False, stream=None):
     """Fill the listed slots of ``pool`` (as in ``kda_state_copy``) with zeros."""
     dev, *args = _pool_args(pool, layered)
     a = _index_list(slots, "slots")
-    _call(dev, stream, load_library().kda_state_clear, "kda_state_clear", *args, a.data_ptr(),
+    _call(dev, stream, "kda_state_clear", *args, a.data_ptr(),
           a.numel())
 
 

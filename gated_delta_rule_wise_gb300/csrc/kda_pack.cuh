@@ -1,0 +1,84 @@
+// kda_pack.cuh -- two float32 values in one 64-bit register pair (sm_103a's
+// packed products and sums issue once for both), and the approximate
+// functions of the elementwise parts.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace kda {
+
+typedef unsigned long long f2;
+
+__device__ __forceinline__ f2 pack(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 both(float x) { return pack(x, x); }
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x, within 2^-22 relative.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// x / (1 + exp(-x)); an exponential past float32's range gives 0.
+__device__ __forceinline__ float silu(float x) { return x * rcp(1.f + ex2(x * -kLog2e)); }
+__device__ __forceinline__ f2 silu2(f2 v) {
+  const float2 t = unpack(mul2(v, both(-kLog2e)));
+  const float2 s = unpack(add2(pack(ex2(t.x), ex2(t.y)), both(1.f)));
+  return mul2(v, pack(rcp(s.x), rcp(s.y)));
+}
+
+// ----- two stored values: as loaded, and as a packed float32 pair
+template <typename TI> struct Two;
+template <> struct Two<__nv_bfloat16> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ raw join(__nv_bfloat16 lo, __nv_bfloat16 hi) {
+    return (uint32_t)__bfloat16_as_ushort(lo) | (uint32_t)__bfloat16_as_ushort(hi) << 16;
+  }
+  static __device__ __forceinline__ f2 widen(raw v) {
+    return pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ raw narrow(f2 v) {
+    const float2 x = unpack(v);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+  }
+};
+template <> struct Two<float> {
+  typedef f2 raw;
+  static __device__ __forceinline__ raw join(float lo, float hi) { return pack(lo, hi); }
+  static __device__ __forceinline__ f2 widen(raw v) { return v; }
+  static __device__ __forceinline__ raw narrow(f2 v) { return v; }
+};
+
+}  // namespace kda

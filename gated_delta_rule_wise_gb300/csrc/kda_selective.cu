@@ -12,18 +12,17 @@
 #include <type_traits>
 
 #include "kda_launch.cuh"
+#include "kda_pack.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kScanThreads = 128;
-constexpr int kPer = 4;  // state entries per thread
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kStepThreads = 256;
+constexpr int kPer = 4;  // state entries per thread of a step
 
 __device__ __forceinline__ float softplus(float x) {
   return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
 }
-__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 struct Rows {  // a strided input: batch and token stride in elements
   const void *p;
@@ -41,39 +40,6 @@ struct ScanArgs {
 
 // ---------------------------------------------------------------- prompts
 
-// Two float32 values in one 64-bit register pair: the packed products and sums
-// below issue once for both.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 constexpr int kMaxSplit = 64;      // parts of a sequence
 constexpr int kTargetWarps = 1216; // 152 SMs x 4 schedulers x 2
 constexpr unsigned kVecU = 1, kVecDelta = 2, kVecB = 4, kVecC = 8, kVecZ = 16;
@@ -87,35 +53,12 @@ struct ScanPlan {
   bool pairs;       // every row of y starts on two values
 };
 
-// ----- two stored values: as loaded, and as a packed float32 pair
-template <typename TI> struct Two;
-template <> struct Two<__nv_bfloat16> {
-  typedef uint32_t raw;
-  static __device__ __forceinline__ raw join(__nv_bfloat16 lo, __nv_bfloat16 hi) {
-    return (uint32_t)__bfloat16_as_ushort(lo) | (uint32_t)__bfloat16_as_ushort(hi) << 16;
-  }
-  static __device__ __forceinline__ f2 widen(raw v) {
-    return pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-  }
-  static __device__ __forceinline__ void st(__nv_bfloat16 *p, f2 v) {
-    const float2 x = unpack(v);
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x.x, x.y);
-  }
-};
-template <> struct Two<float> {
-  typedef f2 raw;
-  static __device__ __forceinline__ raw join(float lo, float hi) { return pack(lo, hi); }
-  static __device__ __forceinline__ f2 widen(raw v) { return v; }
-  static __device__ __forceinline__ void st(float *p, f2 v) { *reinterpret_cast<f2 *>(p) = v; }
-};
 // n (0, 1, 2) values from p on; `wide`: both in one load.  What is missing is zero.
 template <typename TI>
 __device__ __forceinline__ typename Two<TI>::raw load_two(const TI *p, int n, bool wide) {
   if (wide) return n > 0 ? *reinterpret_cast<const typename Two<TI>::raw *>(p) : 0;
   return Two<TI>::join(n > 0 ? p[0] : TI(0.f), n > 1 ? p[1] : TI(0.f));
 }
-__device__ __forceinline__ f2 both(float x) { return pack(x, x); }
-
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  The argument's
 // rounding is put back into e (its residual is exact in one fma).  log1p(e) / e
 // is a polynomial of degree 9, the least relative maximum error on [0, 1]
@@ -501,14 +444,12 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     for (int i = 0; i < kTimes; ++i) {
       if (kRows * kTimes != TT && tr >= TT) break;
       v[i] = fma2(skip, Two<TI>::widen(ru[i]), *reinterpret_cast<const f2 *>(sy + i * kRows * CT));
-      if (gated) {
-        const float2 gate = unpack(Two<TI>::widen(rz[i]));
-        v[i] = mul2(v[i], pack(silu(gate.x), silu(gate.y)));
-      }
+      if (gated) v[i] = mul2(v[i], silu2(Two<TI>::widen(rz[i])));
     }
     if (p.pairs && rows >= TT && two == 2 && kRows * kTimes == TT) {
 #pragma unroll
-      for (int i = 0; i < kTimes; ++i) Two<TI>::st(y + i * y_step, v[i]);
+      for (int i = 0; i < kTimes; ++i)
+        *reinterpret_cast<raw2 *>(y + i * y_step) = Two<TI>::narrow(v[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < kTimes; ++i) {
@@ -542,45 +483,74 @@ struct StepArgs {
   int n_slots;
   void *y;
   int R, D, G, softplus;
+  int rows;  // rows of a thread
+  unsigned cblocks;
 };
 
+// A group of L lanes takes a channel of `rows` rows: each lane keeps its four
+// entries of A for them and reads two rows' states before it writes either.
 template <typename TI, int N>
-__global__ void __launch_bounds__(kScanThreads) selective_step_kernel(StepArgs a) {
-  constexpr int L = N / kPer;
-  const long long id = (long long)blockIdx.x * (kScanThreads / L) + threadIdx.x / L;
+__global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const StepArgs a) {
+  constexpr int L = N / kPer, kChans = kStepThreads / L;
   const int lane = threadIdx.x % L;
-  if (id >= (long long)a.R * a.D) return;  // a whole group leaves at once
-  const int r = (int)(id / a.D), c = (int)(id % a.D);
-  const int slot = a.slots ? a.slots[r] : r;
-  if (slot < 0 || slot >= a.n_slots) return;
+  const int c = blockIdx.x % a.cblocks * kChans + threadIdx.x / L;
+  const long long r0 = (long long)(blockIdx.x / a.cblocks) * a.rows;
+  if (c >= a.D) return;  // a whole group leaves at once
   const int g = c / (a.D / a.G);
-  float *S = a.S + ((long long)slot * a.D + c) * N + lane * kPer;
-  const float ut = Io<TI>::ld(static_cast<const TI *>(a.u.p) + r * a.u.sb + c);
-  float dt = Io<TI>::ld(static_cast<const TI *>(a.delta.p) + r * a.delta.sb + c) +
-             (a.bias ? a.bias[c] : 0.f);
-  if (a.softplus) dt = softplus(dt);
-  const TI *Bm = static_cast<const TI *>(a.Bm.p) + r * a.Bm.sb + (long long)g * N + lane * kPer;
-  const TI *Cm = static_cast<const TI *>(a.Cm.p) + r * a.Cm.sb + (long long)g * N + lane * kPer;
-  float acc = 0.f;
+  float4 A = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + lane * kPer);
+  const f2 A01 = pack(A.x * kLog2e, A.y * kLog2e), A23 = pack(A.z * kLog2e, A.w * kLog2e);
+  const float bias = a.bias ? a.bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
+  const unsigned group = ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
+  const int r1 = (int)min((long long)a.R, r0 + a.rows);
+  constexpr int kTwo = 2;
+#pragma unroll 1
+  for (int r = (int)r0; r < r1; r += kTwo) {
+    float4 s[kTwo];
+    float *S[kTwo];
+    float u[kTwo], dt[kTwo], z[kTwo], Bv[kTwo][4], Cv[kTwo][4];
+    bool live[kTwo];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const float A2 = a.A[(long long)c * N + lane * kPer + k] * kLog2e;
-    const float h = exp2f(dt * A2) * S[k] + dt * ut * Io<TI>::ld(Bm + k);
-    S[k] = h;
-    acc += h * Io<TI>::ld(Cm + k);
-  }
-  const unsigned mask = ((L == 32 ? 0u : (1u << (L & 31))) - 1u) << (threadIdx.x % 32 / L * L);
+    for (int i = 0; i < kTwo; ++i) {
+      const int slot = r + i >= r1 ? -1 : a.slots ? a.slots[r + i] : r + i;
+      live[i] = slot >= 0 && slot < a.n_slots;
+      if (!live[i]) continue;
+      const long long row = r + i;
+      S[i] = a.S + ((long long)slot * a.D + c) * N + lane * kPer;
+      s[i] = *reinterpret_cast<const float4 *>(S[i]);
+      u[i] = Io<TI>::ld(static_cast<const TI *>(a.u.p) + row * a.u.sb + c);
+      dt[i] = Io<TI>::ld(static_cast<const TI *>(a.delta.p) + row * a.delta.sb + c);
+      z[i] = a.z.p ? Io<TI>::ld(static_cast<const TI *>(a.z.p) + row * a.z.sb + c) : 0.f;
+      const TI *B = static_cast<const TI *>(a.Bm.p) + row * a.Bm.sb + (long long)g * N + lane * kPer;
+      const TI *C = static_cast<const TI *>(a.Cm.p) + row * a.Cm.sb + (long long)g * N + lane * kPer;
 #pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(mask, acc, off);
-  if (lane == 0) {
-    if (a.Dskip) acc += a.Dskip[c] * ut;
-    if (a.z.p) acc *= silu(Io<TI>::ld(static_cast<const TI *>(a.z.p) + r * a.z.sb + c));
-    Io<TI>::st(static_cast<TI *>(a.y) + id, acc);
+      for (int k = 0; k < 4; ++k) Bv[i][k] = Io<TI>::ld(B + k), Cv[i][k] = Io<TI>::ld(C + k);
+    }
+#pragma unroll
+    for (int i = 0; i < kTwo; ++i) {
+      if (!live[i]) continue;
+      float d = dt[i] + bias;
+      if (a.softplus) d = softplus(d);
+      const float2 e0 = unpack(mul2(A01, both(d))), e1 = unpack(mul2(A23, both(d)));
+      const f2 x = both(d * u[i]);
+      const f2 h0 = fma2(pack(ex2(e0.x), ex2(e0.y)), pack(s[i].x, s[i].y), mul2(x, pack(Bv[i][0], Bv[i][1])));
+      const f2 h1 = fma2(pack(ex2(e1.x), ex2(e1.y)), pack(s[i].z, s[i].w), mul2(x, pack(Bv[i][2], Bv[i][3])));
+      const float2 v0 = unpack(h0), v1 = unpack(h1);
+      *reinterpret_cast<float4 *>(S[i]) = make_float4(v0.x, v0.y, v1.x, v1.y);
+      const float2 w = unpack(fma2(h1, pack(Cv[i][2], Cv[i][3]), mul2(h0, pack(Cv[i][0], Cv[i][1]))));
+      float y = w.x + w.y;
+#pragma unroll
+      for (int off = L / 2; off > 0; off >>= 1) y += __shfl_xor_sync(group, y, off);
+      if (lane == 0) {
+        y = fmaf(skip, u[i], y);
+        if (a.z.p) y *= silu(z[i]);
+        Io<TI>::st(static_cast<TI *>(a.y) + (long long)(r + i) * a.D + c, y);
+      }
+    }
   }
 }
 
 struct ScanChoice {
-  int cut, split;
+  int cut, split;  // which Cut, parts of a sequence
 };
 // Two channels per lane group halve the reads of B and C per entry, and the warps: worth it
 // once the state alone fills the schedulers (8192 channels of 16 entries: 129 against 133 us
@@ -626,11 +596,14 @@ kda_status launch_scan(const ScanArgs &a, const ScanPlan &p, int cut, cudaStream
   return launch_scan_cut<TI, N, Cut<1, 4, 128, 128>>(a, p, st);
 }
 template <typename TI, int N>
-kda_status launch_step(const StepArgs &a, cudaStream_t st) {
-  const long long per = kScanThreads / (N / kPer);
-  const long long blocks = ((long long)a.R * a.D + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  selective_step_kernel<TI, N><<<(unsigned)blocks, kScanThreads, 0, st>>>(a);
+kda_status launch_step(StepArgs a, cudaStream_t st) {
+  constexpr int kChans = kStepThreads / (N / kPer);
+  a.cblocks = (unsigned)(((long long)a.D + kChans - 1) / kChans);
+  const auto blocks = [&] { return (long long)a.cblocks * ((a.R + a.rows - 1) / a.rows); };
+  a.rows = 4;  // fewer where that would leave SMs without four CTAs
+  while (a.rows > 1 && blocks() < 152 * 4) a.rows /= 2;
+  if (blocks() > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  selective_step_kernel<TI, N><<<(unsigned)blocks(), kStepThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -753,7 +726,7 @@ extern "C" kda_status kda_selective_step(const void *u, const void *delta, const
   const StepArgs a{{u, strides[0], 0}, {delta, strides[1], 0}, {Bm, strides[2], 0},
                    {Cm, strides[3], 0}, {z, z ? strides[4] : 0, 0},
                    A, Dskip, delta_bias, S, slots, n_slots, y, R, D, G,
-                   (flags & KDA_SCAN_SOFTPLUS) != 0u};
+                   (flags & KDA_SCAN_SOFTPLUS) != 0u, 0, 0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_step_n<__nv_bfloat16>(a, N, st) : launch_step_n<float>(a, N, st);
 }

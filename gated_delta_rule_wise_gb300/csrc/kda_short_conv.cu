@@ -8,14 +8,38 @@
 #include <stdint.h>
 
 #include "kda_launch.cuh"
+#include "kda_pack.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kConvThreads = 128;
+constexpr int kInFlight = 8;  // tokens a thread reads ahead of its products
 
-__device__ __forceinline__ float conv_act(float v, int silu) {
-  return silu ? v / (1.f + expf(-v)) : v;
+// V neighbouring channels of one token (16 bytes, 2 values or 1), as loaded.
+template <typename TI, int V> struct Chunk;
+template <int V> struct Chunk<__nv_bfloat16, V> {
+  uint32_t r[V / 2];
+};
+template <int V> struct Chunk<float, V> {
+  f2 r[V / 2];
+};
+template <typename TI, int V> __device__ __forceinline__ Chunk<TI, V> load_chunk(const TI *p) {
+  Chunk<TI, V> c;
+  if (V * sizeof(TI) == 16) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    c = *reinterpret_cast<const Chunk<TI, V> *>(&v);
+  } else {
+    c.r[0] = *reinterpret_cast<const typename Two<TI>::raw *>(p);
+  }
+  return c;
+}
+template <typename TI, int V>
+__device__ __forceinline__ void store_chunk(TI *p, const Chunk<TI, V> &c) {
+  if (V * sizeof(TI) == 16)
+    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&c);
+  else
+    *reinterpret_cast<typename Two<TI>::raw *>(p) = c.r[0];
 }
 
 struct ConvArgs {
@@ -26,40 +50,170 @@ struct ConvArgs {
   const int *lens;
   void *y, *sT;
   int B, H, T, d, silu;
+  int cx;   // threads of a CTA side by side on channels (a power of two)
+  int run;  // tokens of a thread
+  long long cblocks, tblocks;
 };
 
-// One thread per (batch row, channel), token after token.
-template <typename TI, int W>
-__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(ConvArgs a) {
-  const long long C = (long long)a.H * a.d;
-  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-  if (id >= C * a.B) return;
-  const int b = (int)(id / C);
-  const int h = (int)(id % C / a.d), i = (int)(id % a.d);
-  const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-  const TI *x = static_cast<const TI *>(a.x) + b * a.x_sb + h * a.x_sh + i;
-  TI *y = static_cast<TI *>(a.y) + ((long long)b * a.H + h) * a.T * a.d + i;
-  const long long so = ((long long)b * a.H + h) * (W - 1) * a.d + i;
-  float w[W], win[W];
+// The taps and the bias of V channels from channel c of the [H d] on, in pairs
+// of channels (of one, its pair's other half is 0).
+template <int W, int V> struct Taps {
+  static constexpr int P = (V + 1) / 2;
+  f2 w[W][P], bias[P];
+  __device__ __forceinline__ void load(const float *pw, const float *pb, long long c) {
+    float t[V][W];
+    if (W == 4) {
 #pragma unroll
-  for (int j = 0; j < W; ++j) w[j] = a.w[((long long)h * a.d + i) * W + j];
-  const float bias = a.bias ? a.bias[(long long)h * a.d + i] : 0.f;
+      for (int v = 0; v < V; ++v) {
+        const float4 q = *reinterpret_cast<const float4 *>(pw + (c + v) * 4);
+        t[v][0] = q.x, t[v][1] = q.y, t[v][2 % W] = q.z, t[v][3 % W] = q.w;
+      }
+    } else {
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    win[j] = a.s0 ? Io<TI>::ld(static_cast<const TI *>(a.s0) + so + (long long)j * a.d) : 0.f;
-  for (int t = 0; t < len; ++t) {
-    win[W - 1] = Io<TI>::ld(x + t * a.x_st);
-    float v = bias;
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < W; ++j) v += w[j] * win[j];
-    Io<TI>::st(y + (long long)t * a.d, conv_act(v, a.silu));
+        for (int j = 0; j < W; ++j) t[v][j] = pw[(c + v) * W + j];
+    }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][i] = pack(t[2 * i][j], V > 1 ? t[(2 * i + 1) % V][j] : 0.f);
+      bias[i] = pb ? pack(pb[c + 2 * i], V > 1 ? pb[c + 2 * i + 1] : 0.f) : 0;
+    }
   }
-  if (a.sT) {
+};
+
+// A chunk as float32 pairs and back; V = 1 goes through plain loads.
+template <typename TI, int V> struct Line {
+  static constexpr int P = (V + 1) / 2;
+  f2 p[P];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = 0;
+  }
+};
+
+template <typename TI, int V> struct Raw {  // what a load returns
+  Chunk<TI, V> c;
+  __device__ __forceinline__ void load(const TI *q) { c = load_chunk<TI, V>(q); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) c.r[i] = 0;
+  }
+  __device__ __forceinline__ void store(TI *q) const { store_chunk<TI, V>(q, c); }
+  __device__ __forceinline__ void widen(Line<TI, V> &l) const {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) l.p[i] = Two<TI>::widen(c.r[i]);
+  }
+  __device__ __forceinline__ void narrow(const Line<TI, V> &l) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) c.r[i] = Two<TI>::narrow(l.p[i]);
+  }
+};
+template <typename TI> struct Raw<TI, 1> {
+  TI c;
+  __device__ __forceinline__ void load(const TI *q) { c = *q; }
+  __device__ __forceinline__ void zero() { c = TI(0.f); }
+  __device__ __forceinline__ void store(TI *q) const { *q = c; }
+  __device__ __forceinline__ void widen(Line<TI, 1> &l) const { l.p[0] = pack(Io<TI>::ld(&c), 0.f); }
+  __device__ __forceinline__ void narrow(const Line<TI, 1> &l) { Io<TI>::st(&c, unpack(l.p[0]).x); }
+};
+
+// One token: W products per channel, the bias, the activation.
+template <typename TI, int W, int V>
+__device__ __forceinline__ void conv_token(const Taps<W, V> &taps, const Line<TI, V> (&win)[W],
+                                           int silu, Line<TI, V> &out) {
+#pragma unroll
+  for (int i = 0; i < Taps<W, V>::P; ++i) {
+    f2 v = taps.bias[i];
+#pragma unroll
+    for (int j = 0; j < W; ++j) v = fma2(taps.w[j][i], win[j].p[i], v);
+    out.p[i] = silu ? silu2(v) : v;
+  }
+}
+
+// A thread takes V channels and `run` tokens: the W - 1 inputs before them stay
+// in registers as they move along, so each input is read once but for the
+// W - 1 at a run's start.
+template <typename TI, int W, int V>
+__global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
+  const int lx = threadIdx.x & (a.cx - 1), ly = threadIdx.x / a.cx;
+  const long long C = (long long)a.H * (a.d / V);
+  const long long cb = blockIdx.x % a.cblocks, rest = blockIdx.x / a.cblocks;
+  const int b = (int)(rest / a.tblocks);
+  const long long t0 = (rest % a.tblocks * (kConvThreads / a.cx) + ly) * a.run;
+  const long long c = cb * a.cx + lx;
+  const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+  if (c >= C || (t0 > 0 && t0 >= len)) return;
+  const int h = (int)(c / (a.d / V)), i0 = (int)(c % (a.d / V)) * V;
+  const long long t1 = min((long long)len, t0 + a.run);
+  const TI *x = static_cast<const TI *>(a.x) + b * a.x_sb + h * a.x_sh + i0;
+  const TI *s0 = static_cast<const TI *>(a.s0);
+  const long long so = ((long long)b * a.H + h) * (W - 1) * a.d + i0;
+
+  Raw<TI, V> past[W - 1];  // the inputs before t0
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const long long t = t0 - (W - 1) + j;
+    if (t >= 0)
+      past[j].load(x + t * a.x_st);
+    else if (s0)
+      past[j].load(s0 + so + (t + W - 1) * a.d);
+    else
+      past[j].zero();
+  }
+  if (t0 == 0 && a.sT) {
+    // The state: the thread that has s0 in registers writes it, so that sT may be s0.
+    Raw<TI, V> last[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const long long t = len - (W - 1) + j;
+      if (t >= 0) {
+        last[j].load(x + t * a.x_st);
+      } else {
+        last[j] = past[0];
+#pragma unroll
+        for (int k = 1; k < W - 1; ++k)
+          if (t + W - 1 == k) last[j] = past[k];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      Io<TI>::st(static_cast<TI *>(a.sT) + so + (long long)j * a.d, win[j]);
+      last[j].store(static_cast<TI *>(a.sT) + so + (long long)j * a.d);
+  }
+  if (t0 >= len) return;
+
+  Taps<W, V> taps;
+  taps.load(a.w, a.bias, (long long)h * a.d + i0);
+  Line<TI, V> win[W];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) past[j].widen(win[j]);
+  TI *y = static_cast<TI *>(a.y) + (((long long)b * a.H + h) * a.T + t0) * a.d + i0;
+  x += t0 * a.x_st;
+  const auto token = [&](const Raw<TI, V> &in, int k) {
+    in.widen(win[W - 1]);
+    Line<TI, V> out;
+    conv_token<TI, W, V>(taps, win, a.silu, out);
+    Raw<TI, V> r;
+    r.narrow(out);
+    r.store(y + (long long)k * a.d);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) win[j] = win[j + 1];
+  };
+  int left = (int)(t1 - t0);
+#pragma unroll 1
+  for (; left >= kInFlight; left -= kInFlight) {
+    Raw<TI, V> in[kInFlight];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) in[k].load(x + k * a.x_st);
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) token(in[k], k);
+    x += kInFlight * a.x_st, y += (long long)kInFlight * a.d;
+  }
+  for (int k = 0; k < left; ++k) {
+    Raw<TI, V> in;
+    in.load(x + k * a.x_st);
+    token(in, k);
   }
 }
 
@@ -72,51 +226,112 @@ struct ConvStepArgs {
   int n_slots;
   void *y;
   int N, H, d, silu;
+  int cx;    // threads of a CTA side by side on channels (a power of two)
+  int rows;  // rows of a thread
+  long long cblocks;
 };
 
-template <typename TI, int W>
-__global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(ConvStepArgs a) {
-  const long long C = (long long)a.H * a.d;
-  const long long id = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-  if (id >= C * a.N) return;
-  const int n = (int)(id / C);
-  const int h = (int)(id % C / a.d), i = (int)(id % a.d);
-  const int slot = a.slots ? a.slots[n] : n;
-  if (slot < 0 || slot >= a.n_slots) return;
-  TI *S = static_cast<TI *>(a.S) + ((long long)slot * a.H + h) * (W - 1) * a.d + i;
-  const float *w = a.w + ((long long)h * a.d + i) * W;
-  float v = a.bias ? a.bias[(long long)h * a.d + i] : 0.f;
-  float win[W];
+// A thread takes V channels of `rows` rows, so that the taps (float32, as many
+// bytes as a bf16 row's input and state) are read once for them.
+template <typename TI, int W, int V>
+__global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const ConvStepArgs a) {
+  const int lx = threadIdx.x & (a.cx - 1), ly = threadIdx.x / a.cx;
+  const long long C = (long long)a.H * (a.d / V);
+  const long long c = blockIdx.x % a.cblocks * a.cx + lx;
+  const long long n0 = (blockIdx.x / a.cblocks * (kConvThreads / a.cx) + ly) * a.rows;
+  if (c >= C || n0 >= a.N) return;
+  const int h = (int)(c / (a.d / V)), i0 = (int)(c % (a.d / V)) * V;
+  Taps<W, V> taps;
+  taps.load(a.w, a.bias, (long long)h * a.d + i0);
+  const int n1 = (int)min((long long)a.N, n0 + a.rows);
+  constexpr int kTwo = 2;  // rows read before either is written
+#pragma unroll 1
+  for (int n = (int)n0; n < n1; n += kTwo) {
+    Raw<TI, V> in[kTwo][W];
+    TI *S[kTwo];
+    bool live[kTwo];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) win[j] = Io<TI>::ld(S + (long long)j * a.d);
-  win[W - 1] = Io<TI>::ld(static_cast<const TI *>(a.x) + n * a.x_sn + h * a.x_sh + i);
+    for (int r = 0; r < kTwo; ++r) {
+      const int slot = n + r >= n1 ? -1 : a.slots ? a.slots[n + r] : n + r;
+      live[r] = slot >= 0 && slot < a.n_slots;
+      S[r] = static_cast<TI *>(a.S) + ((long long)(live[r] ? slot : 0) * a.H + h) * (W - 1) * a.d + i0;
+      if (!live[r]) continue;
 #pragma unroll
-  for (int j = 0; j < W; ++j) v += w[j] * win[j];
-  Io<TI>::st(static_cast<TI *>(a.y) + id, conv_act(v, a.silu));
+      for (int j = 0; j < W - 1; ++j) in[r][j].load(S[r] + (long long)j * a.d);
+      in[r][W - 1].load(static_cast<const TI *>(a.x) + (n + r) * a.x_sn + h * a.x_sh + i0);
+    }
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) Io<TI>::st(S + (long long)j * a.d, win[j + 1]);
+    for (int r = 0; r < kTwo; ++r) {
+      if (!live[r]) continue;
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) in[r][j + 1].store(S[r] + (long long)j * a.d);
+      Line<TI, V> win[W], out;
+#pragma unroll
+      for (int j = 0; j < W; ++j) in[r][j].widen(win[j]);
+      conv_token<TI, W, V>(taps, win, a.silu, out);
+      Raw<TI, V> v;
+      v.narrow(out);
+      v.store(static_cast<TI *>(a.y) + ((long long)(n + r) * a.H + h) * a.d + i0);
+    }
+  }
 }
 
-template <typename TI>
-kda_status launch_conv(const ConvArgs &a, int W, cudaStream_t st) {
-  const long long blocks = ((long long)a.B * a.H * a.d + kConvThreads - 1) / kConvThreads;
-  if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  const unsigned g = (unsigned)blocks;
-  if (W == 2) short_conv_kernel<TI, 2><<<g, kConvThreads, 0, st>>>(a);
-  if (W == 3) short_conv_kernel<TI, 3><<<g, kConvThreads, 0, st>>>(a);
-  if (W == 4) short_conv_kernel<TI, 4><<<g, kConvThreads, 0, st>>>(a);
+int pow2_up(long long n) {  // the power of two from n on, at most a CTA's threads
+  int p = 1;
+  while (p < n && p < kConvThreads) p *= 2;
+  return p;
+}
+
+template <typename TI, int V> kda_status launch_conv(ConvArgs a, int W, cudaStream_t st) {
+  const long long C = (long long)a.H * (a.d / V);
+  a.cx = pow2_up(C);
+  a.cblocks = (C + a.cx - 1) / a.cx;
+  // A run of 32 tokens reads W - 1 twice and its taps once (as many bytes as 4 to 8 tokens);
+  // shorter runs where 32 would leave SMs without four CTAs.
+  a.run = 32;
+  const auto blocks = [&] {
+    const long long per = (long long)a.run * (kConvThreads / a.cx);
+    a.tblocks = a.T > 0 ? (a.T + per - 1) / per : 1;
+    return a.cblocks * a.tblocks * a.B;
+  };
+  while (a.run > kInFlight && blocks() < 152 * 4) a.run /= 2;
+  const long long n = blocks();
+  if (n > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  const unsigned g = (unsigned)n;
+  if (W == 2) short_conv_kernel<TI, 2, V><<<g, kConvThreads, 0, st>>>(a);
+  if (W == 3) short_conv_kernel<TI, 3, V><<<g, kConvThreads, 0, st>>>(a);
+  if (W == 4) short_conv_kernel<TI, 4, V><<<g, kConvThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-template <typename TI>
-kda_status launch_conv_step(const ConvStepArgs &a, int W, cudaStream_t st) {
-  const long long blocks = ((long long)a.N * a.H * a.d + kConvThreads - 1) / kConvThreads;
-  if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  const unsigned g = (unsigned)blocks;
-  if (W == 2) short_conv_step_kernel<TI, 2><<<g, kConvThreads, 0, st>>>(a);
-  if (W == 3) short_conv_step_kernel<TI, 3><<<g, kConvThreads, 0, st>>>(a);
-  if (W == 4) short_conv_step_kernel<TI, 4><<<g, kConvThreads, 0, st>>>(a);
+template <typename TI, int V> kda_status launch_conv_step(ConvStepArgs a, int W, cudaStream_t st) {
+  const long long C = (long long)a.H * (a.d / V);
+  a.cx = pow2_up(C);
+  a.cblocks = (C + a.cx - 1) / a.cx;
+  const auto blocks = [&] {
+    const long long per = (long long)a.rows * (kConvThreads / a.cx);
+    return a.cblocks * ((a.N + per - 1) / per);
+  };
+  a.rows = 4;  // fewer where that would leave SMs without four CTAs
+  while (a.rows > 1 && blocks() < 152 * 4) a.rows /= 2;
+  const long long n = blocks();
+  if (n > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  const unsigned g = (unsigned)n;
+  if (W == 2) short_conv_step_kernel<TI, 2, V><<<g, kConvThreads, 0, st>>>(a);
+  if (W == 3) short_conv_step_kernel<TI, 3, V><<<g, kConvThreads, 0, st>>>(a);
+  if (W == 4) short_conv_step_kernel<TI, 4, V><<<g, kConvThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+// Channels per thread: the most that divide d and to which x's address and
+// strides are aligned (y and the states are dense, so d decides for them).
+int chunk_of(kda_dtype dt, int d, const void *x, long long s0, long long s1, long long s2) {
+  const int e = dt == KDA_BF16 ? 2 : 4;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(x) | (uintptr_t)(s0 * e) |
+                        (uintptr_t)(s1 * e) | (uintptr_t)(s2 * e);
+  if (d % (16 / e) == 0 && all % 16 == 0) return 16 / e;
+  if (d % 2 == 0 && all % (2 * e) == 0) return 2;
+  return 1;
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -141,9 +356,17 @@ extern "C" kda_status kda_short_conv(const void *x, long long x_sb, long long x_
   if (!aligned(x, size_of(dt)) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(s0, 16) ||
       !aligned(lens, 4) || !aligned(y, 16) || !aligned(sT, 16))
     return KDA_ERR_INVALID_ARG;
-  const ConvArgs a{x, x_sb, x_sh, x_st, w, bias, s0, lens, y, sT, B, H, T, d, act == KDA_ACT_SILU};
+  const ConvArgs a{x,  x_sb, x_sh, x_st, w, bias, s0, lens, y, sT, B, H, T, d, act == KDA_ACT_SILU,
+                   0,  0,    0,    0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dt == KDA_BF16 ? launch_conv<__nv_bfloat16>(a, W, st) : launch_conv<float>(a, W, st);
+  const int V = chunk_of(dt, d, x, x_sb, x_sh, x_st);
+  if (dt == KDA_BF16)
+    return V == 8   ? launch_conv<__nv_bfloat16, 8>(a, W, st)
+           : V == 2 ? launch_conv<__nv_bfloat16, 2>(a, W, st)
+                    : launch_conv<__nv_bfloat16, 1>(a, W, st);
+  return V == 4   ? launch_conv<float, 4>(a, W, st)
+         : V == 2 ? launch_conv<float, 2>(a, W, st)
+                  : launch_conv<float, 1>(a, W, st);
 }
 
 extern "C" kda_status kda_short_conv_step(const void *x, long long x_sn, long long x_sh,
@@ -162,8 +385,15 @@ extern "C" kda_status kda_short_conv_step(const void *x, long long x_sn, long lo
   if (!aligned(x, size_of(dt)) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(S, 16) ||
       !aligned(slots, 4) || !aligned(y, 16))
     return KDA_ERR_INVALID_ARG;
-  const ConvStepArgs a{x, x_sn, x_sh, w, bias, S, slots, n_slots, y, N, H, d, act == KDA_ACT_SILU};
+  const ConvStepArgs a{x, x_sn, x_sh, w, bias, S, slots, n_slots, y, N, H, d, act == KDA_ACT_SILU,
+                       0, 0,    0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dt == KDA_BF16 ? launch_conv_step<__nv_bfloat16>(a, W, st)
-                        : launch_conv_step<float>(a, W, st);
+  const int V = chunk_of(dt, d, x, x_sn, x_sh, 0);
+  if (dt == KDA_BF16)
+    return V == 8   ? launch_conv_step<__nv_bfloat16, 8>(a, W, st)
+           : V == 2 ? launch_conv_step<__nv_bfloat16, 2>(a, W, st)
+                    : launch_conv_step<__nv_bfloat16, 1>(a, W, st);
+  return V == 4   ? launch_conv_step<float, 4>(a, W, st)
+         : V == 2 ? launch_conv_step<float, 2>(a, W, st)
+                  : launch_conv_step<float, 1>(a, W, st);
 }
