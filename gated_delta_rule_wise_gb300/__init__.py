@@ -466,8 +466,9 @@ def short_conv(x, w, bias=None, s0=None, lens=None, act=KDA_ACT_SILU, output_fin
     returns (y, sT or None).  With ``lens`` the rows of a new y behind a
     sequence's length hold nothing."""
     B, H, T, d = x.shape
-    y = x.new_empty((B, H, T, d)) if out is None else out
-    sT = x.new_empty((B, H, w.shape[-1] - 1, d)) if output_final_state else None
+    y = torch.empty((B, H, T, d), dtype=x.dtype, device=x.device) if out is None else out
+    sT = (torch.empty((B, H, w.shape[-1] - 1, d), dtype=x.dtype, device=x.device)
+          if output_final_state else None)
     kda_short_conv(x, w, bias, s0, lens, y, sT, act, stream)
     if stream is not None:
         _keep(stream, y, sT)
@@ -493,7 +494,7 @@ def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
 
 def short_conv_step(x, w, S, bias=None, slots=None, act=KDA_ACT_SILU, out=None, stream=None):
     """Allocate y (unless ``out`` is given) and run ``kda_short_conv_step``; returns y."""
-    y = x.new_empty(x.shape) if out is None else out
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
     kda_short_conv_step(x, w, bias, S, slots, y, act, stream)
     if stream is not None:
         _keep(stream, y)
@@ -510,7 +511,7 @@ def selective_scan_workspace_for(u, A, B):
                                           A.shape[1], _dtype_code(u))
     if n == 0:
         raise KdaError(KDA_ERR_UNSUPPORTED, "kda_selective_scan_workspace_size")
-    return u.new_empty(n, dtype=torch.uint8)
+    return torch.empty(n, dtype=torch.uint8, device=u.device)
 
 
 def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, workspace,
@@ -544,8 +545,9 @@ def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, 
     """Allocate y (unless ``out`` is given), hT and the workspace and run
     ``kda_selective_scan``; returns (y, hT or None).  With ``lens`` the rows of
     a new y behind a sequence's length hold nothing."""
-    y = u.new_empty(u.shape) if out is None else out
-    hT = A.new_empty((u.shape[0],) + A.shape) if output_final_state else None
+    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
+    hT = (torch.empty((u.shape[0],) + A.shape, dtype=torch.float32, device=u.device)
+          if output_final_state else None)
     ws = selective_scan_workspace_for(u, A, B) if workspace is None else workspace
     kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, ws, softplus, stream)
     if stream is not None:
@@ -578,7 +580,7 @@ def kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplu
 def selective_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, slots=None,
                    softplus=True, out=None, stream=None):
     """Allocate y (unless ``out`` is given) and run ``kda_selective_step``; returns y."""
-    y = u.new_empty(u.shape) if out is None else out
+    y = torch.empty(u.shape, dtype=u.dtype, device=u.device) if out is None else out
     kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplus, stream)
     if stream is not None:
         _keep(stream, y)
@@ -594,7 +596,8 @@ def _index_list(ix, name):
             raise ValueError(f"{name} must be a list or a one-dimensional integer CPU tensor")
         if ix.dtype == torch.int64 and ix.numel() and (ix.min() < -2**31 or ix.max() >= 2**31):
             raise ValueError(f"{name} holds an index outside 32 bits")
-        return ix.to(torch.int32).contiguous()
+        return ix if ix.dtype == torch.int32 and ix.is_contiguous() else \
+            ix.to(torch.int32).contiguous()
     return torch.tensor(ix, dtype=torch.int32)
 
 
@@ -604,16 +607,12 @@ def _pool_args(pool, layered):
     dev = _device_of(pool, "pool")
     if pool.dim() < (2 if layered else 1):
         raise ValueError("pool has too few axes")
-    one = pool[0] if layered and pool.shape[0] else pool
-    if not one.is_contiguous():
+    if not pool.is_contiguous() and not (layered and pool.shape[0] and pool[0].is_contiguous()):
         raise ValueError("the slots of a pool must be contiguous")
     e = pool.element_size()
-    if not layered:
-        n = pool.shape[0]
-        return dev, pool.data_ptr(), 1, 0, n, (pool.numel() // n * e if n else 0)
-    L, n = pool.shape[0], pool.shape[1]
-    per = pool.numel() // (L * n) * e if L * n else 0
-    return dev, pool.data_ptr(), L, pool.stride(0) * e if L > 1 else 0, n, per
+    L, n = pool.shape[:2] if layered else (1, pool.shape[0])
+    slot = pool.numel() // (L * n) * e if L * n else 0
+    return dev, pool.data_ptr(), L, pool.stride(0) * e if L > 1 else 0, n, slot
 
 
 def kda_state_copy(pool, src, dst, layered=False, stream=None):

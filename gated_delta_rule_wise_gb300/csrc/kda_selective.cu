@@ -569,6 +569,12 @@ ScanChoice scan_choice(int B, int T, int D, int N) {
   return c;
 }
 
+template <class K> bool allow_smem(K *kernel, int bytes) {  // 48 KiB need no leave
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+             cudaSuccess;
+}
+
 template <typename TI, int N, class X>
 kda_status launch_scan_cut(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
   using So = ScanShape<N, X, true>;
@@ -576,13 +582,9 @@ kda_status launch_scan_cut(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
   p.tiles_g = (a.D / a.G + So::CT - 1) / So::CT;
   const long long blocks = (long long)a.B * a.G * p.tiles_g;
   if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(selective_scan_kernel<TI, N, X, true>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, So::kSmem) != cudaSuccess)
-    return KDA_ERR_CUDA;
+  if (!allow_smem(selective_scan_kernel<TI, N, X, true>, So::kSmem)) return KDA_ERR_CUDA;
   if (p.split > 1) {
-    if (cudaFuncSetAttribute(selective_scan_kernel<TI, N, X, false>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Ss::kSmem) != cudaSuccess)
-      return KDA_ERR_CUDA;
+    if (!allow_smem(selective_scan_kernel<TI, N, X, false>, Ss::kSmem)) return KDA_ERR_CUDA;
     selective_scan_kernel<TI, N, X, false>
         <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
   }

@@ -36,8 +36,8 @@ template <typename TI, int V> __device__ __forceinline__ Chunk<TI, V> load_chunk
 }
 template <typename TI, int V>
 __device__ __forceinline__ void store_chunk(TI *p, const Chunk<TI, V> &c) {
-  if (V * sizeof(TI) == 16)
-    *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(&c);
+  if (V * sizeof(TI) == 16)  // written once and read by another kernel: first to leave L2
+    __stcs(reinterpret_cast<uint4 *>(p), *reinterpret_cast<const uint4 *>(&c));
   else
     *reinterpret_cast<typename Two<TI>::raw *>(p) = c.r[0];
 }
@@ -58,27 +58,54 @@ struct ConvArgs {
 // The taps and the bias of V channels from channel c of the [H d] on, in pairs
 // of channels (of one, its pair's other half is 0).
 template <int W, int V> struct Taps {
-  static constexpr int P = (V + 1) / 2;
+  static constexpr int P = (V + 1) / 2, kFours = V * W / 4;
+  // Four taps of eight channels are 128 bytes: lanes that read their own would
+  // touch 32 lines with each load.  The lanes of a warp with neighbouring
+  // chunks read their taps together instead and trade them through shared
+  // memory, where the swizzle keeps both sides free of bank conflicts.
+  static constexpr bool kTrade = W == 4 && V >= 4;
+  static constexpr int kShared = kTrade ? kConvThreads * V : 1;  // float4
   f2 w[W][P], bias[P];
-  __device__ __forceinline__ void load(const float *pw, const float *pb, long long c) {
-    float t[V][W];
-    if (W == 4) {
+
+  // c: this lane's first channel; left: channels from the warp's first to the last
+  __device__ __forceinline__ void load(const float *pw, const float *pb, long long c, bool live,
+                                       bool trade, long long left, float4 *shared) {
+    float t[V * W];
+    if (kTrade && trade) {
+      const int lane = threadIdx.x % 32;
+      float4 *own = shared + threadIdx.x / 32 * 32 * V;
+      const float4 *from = reinterpret_cast<const float4 *>(pw) + (c - (long long)lane * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int q = lane + 32 * i;
+        if (q < left) own[q ^ (q >> 3 & (V - 1))] = from[q];
+      }
+      __syncwarp();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float4 q = *reinterpret_cast<const float4 *>(pw + (c + v) * 4);
-        t[v][0] = q.x, t[v][1] = q.y, t[v][2 % W] = q.z, t[v][3 % W] = q.w;
+        const int q = lane * V + v;
+        const float4 x = own[q ^ (q >> 3 & (V - 1))];
+        t[v * W] = x.x, t[v * W + 1] = x.y, t[(v * W + 2) % (V * W)] = x.z;
+        t[(v * W + 3) % (V * W)] = x.w;
       }
-    } else {
+    } else if (live) {
+      if (V * W % 4 == 0) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+        for (int i = 0; i < kFours; ++i) {
+          const float4 x = reinterpret_cast<const float4 *>(pw + c * W)[i];
+          t[i * 4] = x.x, t[i * 4 + 1] = x.y, t[i * 4 + 2] = x.z, t[i * 4 + 3] = x.w;
+        }
+      } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) t[v][j] = pw[(c + v) * W + j];
+        for (int i = 0; i < V * W; ++i) t[i] = pw[c * W + i];
+      }
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) w[j][i] = pack(t[2 * i][j], V > 1 ? t[(2 * i + 1) % V][j] : 0.f);
-      bias[i] = pb ? pack(pb[c + 2 * i], V > 1 ? pb[c + 2 * i + 1] : 0.f) : 0;
+      for (int j = 0; j < W; ++j)
+        w[j][i] = pack(t[2 * i * W + j], V > 1 ? t[((2 * i + 1) * W + j) % (V * W)] : 0.f);
+      bias[i] = pb && live ? pack(pb[c + 2 * i], V > 1 ? pb[c + 2 * i + 1] : 0.f) : 0;
     }
   }
 };
@@ -144,6 +171,10 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   const long long t0 = (rest % a.tblocks * (kConvThreads / a.cx) + ly) * a.run;
   const long long c = cb * a.cx + lx;
   const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+  Taps<W, V> taps;
+  __shared__ float4 shared[Taps<W, V>::kShared];
+  if (a.cx >= 32 && t0 > 0 && t0 >= len) return;  // (a warp's lanes share t0)
+  taps.load(a.w, a.bias, c * V, c < C, a.cx >= 32, (C - (c - threadIdx.x % 32)) * V, shared);
   if (c >= C || (t0 > 0 && t0 >= len)) return;
   const int h = (int)(c / (a.d / V)), i0 = (int)(c % (a.d / V)) * V;
   const long long t1 = min((long long)len, t0 + a.run);
@@ -183,8 +214,6 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs
   }
   if (t0 >= len) return;
 
-  Taps<W, V> taps;
-  taps.load(a.w, a.bias, (long long)h * a.d + i0);
   Line<TI, V> win[W];
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) past[j].widen(win[j]);
@@ -239,10 +268,12 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const Con
   const long long C = (long long)a.H * (a.d / V);
   const long long c = blockIdx.x % a.cblocks * a.cx + lx;
   const long long n0 = (blockIdx.x / a.cblocks * (kConvThreads / a.cx) + ly) * a.rows;
+  Taps<W, V> taps;
+  __shared__ float4 shared[Taps<W, V>::kShared];
+  if (a.cx >= 32 && n0 >= a.N) return;  // (a warp's lanes share n0)
+  taps.load(a.w, a.bias, c * V, c < C, a.cx >= 32, (C - (c - threadIdx.x % 32)) * V, shared);
   if (c >= C || n0 >= a.N) return;
   const int h = (int)(c / (a.d / V)), i0 = (int)(c % (a.d / V)) * V;
-  Taps<W, V> taps;
-  taps.load(a.w, a.bias, (long long)h * a.d + i0);
   const int n1 = (int)min((long long)a.N, n0 + a.rows);
   constexpr int kTwo = 2;  // rows read before either is written
 #pragma unroll 1
