@@ -17,12 +17,7 @@
 namespace kda {
 namespace {
 
-constexpr int kStepThreads = 256;
-constexpr int kPer = 4;  // state entries per thread of a step
-
-__device__ __forceinline__ float softplus(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-}
+constexpr int kStepThreads = 128;
 
 struct Rows {  // a strided input: batch and token stride in elements
   const void *p;
@@ -483,69 +478,86 @@ struct StepArgs {
   int n_slots;
   void *y;
   int R, D, G, softplus;
-  int rows;  // rows of a thread
+  unsigned vec;  // of B and C, as in ScanPlan
   unsigned cblocks;
 };
 
-// A group of L lanes takes a channel of `rows` rows: each lane keeps its four
-// entries of A for them and reads two rows' states before it writes either.
+// Four values of B or C from p on, in one load where they are aligned.
+template <typename TI> struct Four {
+  typename Two<TI>::raw v[2];
+  __device__ __forceinline__ void load(const TI *p, bool wide) {
+    if (wide) {
+      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
+      const four w = *reinterpret_cast<const four *>(p);
+      v[0] = w.x, v[1] = w.y;
+    } else {
+      v[0] = load_two<TI>(p, 2, false), v[1] = load_two<TI>(p + 2, 2, false);
+    }
+  }
+  __device__ __forceinline__ f2 pair(int i) const { return Two<TI>::widen(v[i]); }
+};
+
+// A group of N / 8 lanes takes one channel of one row; a lane's entries are the
+// four from 4 lane on and the four from N / 2 + 4 lane on, so that a group's
+// reads are whole sectors.  HBM bounds it: each state is read and written once,
+// with streaming accesses (a state comes back a token later at the earliest).
+// Eight entries per lane because what a row costs besides them (addresses,
+// softplus, the gate) is every lane's: at four, issue held the kernel back (256
+// rows x 4096 channels x 16: 47 us against 31), at sixteen too few reads are in
+// flight (37 us).  Two or four rows per thread, to read A once for them, are no
+// faster (31 and 39 us): A comes from L2.
 template <typename TI, int N>
 __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const StepArgs a) {
-  constexpr int L = N / kPer, kChans = kStepThreads / L;
+  constexpr int L = N / 8, kChans = kStepThreads / L;
   const int lane = threadIdx.x % L;
   const int c = blockIdx.x % a.cblocks * kChans + threadIdx.x / L;
-  const long long r0 = (long long)(blockIdx.x / a.cblocks) * a.rows;
+  const long long r = blockIdx.x / a.cblocks;
   if (c >= a.D) return;  // a whole group leaves at once
-  const int g = c / (a.D / a.G);
-  float4 A = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + lane * kPer);
-  const f2 A01 = pack(A.x * kLog2e, A.y * kLog2e), A23 = pack(A.z * kLog2e, A.w * kLog2e);
-  const float bias = a.bias ? a.bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
-  const unsigned group = ((1u << L) - 1u) << (threadIdx.x % 32 / L * L);
-  const int r1 = (int)min((long long)a.R, r0 + a.rows);
-  constexpr int kTwo = 2;
-#pragma unroll 1
-  for (int r = (int)r0; r < r1; r += kTwo) {
-    float4 s[kTwo];
-    float *S[kTwo];
-    float u[kTwo], dt[kTwo], z[kTwo], Bv[kTwo][4], Cv[kTwo][4];
-    bool live[kTwo];
+  const int slot = a.slots ? a.slots[r] : (int)r;
+  if (slot < 0 || slot >= a.n_slots) return;
+  const long long e = (long long)c * N + lane * 4;
+  const long long n = (long long)(c / (a.D / a.G)) * N + lane * 4;
+  float *S = a.S + (long long)slot * a.D * N + e;
+  const TI *pB = static_cast<const TI *>(a.Bm.p) + r * a.Bm.sb + n;
+  const TI *pC = static_cast<const TI *>(a.Cm.p) + r * a.Cm.sb + n;
+  const bool gated = a.z.p != nullptr;
+  float4 s[2], A[2];
+  Four<TI> B[2], C[2];
 #pragma unroll
-    for (int i = 0; i < kTwo; ++i) {
-      const int slot = r + i >= r1 ? -1 : a.slots ? a.slots[r + i] : r + i;
-      live[i] = slot >= 0 && slot < a.n_slots;
-      if (!live[i]) continue;
-      const long long row = r + i;
-      S[i] = a.S + ((long long)slot * a.D + c) * N + lane * kPer;
-      s[i] = *reinterpret_cast<const float4 *>(S[i]);
-      u[i] = Io<TI>::ld(static_cast<const TI *>(a.u.p) + row * a.u.sb + c);
-      dt[i] = Io<TI>::ld(static_cast<const TI *>(a.delta.p) + row * a.delta.sb + c);
-      z[i] = a.z.p ? Io<TI>::ld(static_cast<const TI *>(a.z.p) + row * a.z.sb + c) : 0.f;
-      const TI *B = static_cast<const TI *>(a.Bm.p) + row * a.Bm.sb + (long long)g * N + lane * kPer;
-      const TI *C = static_cast<const TI *>(a.Cm.p) + row * a.Cm.sb + (long long)g * N + lane * kPer;
+  for (int q = 0; q < 2; ++q) s[q] = __ldcs(reinterpret_cast<const float4 *>(S + q * (N / 2)));
+  const float u = Io<TI>::ld(static_cast<const TI *>(a.u.p) + r * a.u.sb + c);
+  float dt = Io<TI>::ld(static_cast<const TI *>(a.delta.p) + r * a.delta.sb + c);
+  const float z = gated ? Io<TI>::ld(static_cast<const TI *>(a.z.p) + r * a.z.sb + c) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) Bv[i][k] = Io<TI>::ld(B + k), Cv[i][k] = Io<TI>::ld(C + k);
-    }
+  for (int q = 0; q < 2; ++q) {
+    B[q].load(pB + q * (N / 2), a.vec & kVecB);
+    C[q].load(pC + q * (N / 2), a.vec & kVecC);
+    A[q] = *reinterpret_cast<const float4 *>(a.A + e + q * (N / 2));
+  }
+  const float skip = a.Dskip ? a.Dskip[c] : 0.f;
+  dt += a.bias ? a.bias[c] : 0.f;
+  if (a.softplus) dt = unpack(softplus2(both(dt))).x;
+  const f2 step = both(dt), xu = both(dt * u);
+  f2 sum;
 #pragma unroll
-    for (int i = 0; i < kTwo; ++i) {
-      if (!live[i]) continue;
-      float d = dt[i] + bias;
-      if (a.softplus) d = softplus(d);
-      const float2 e0 = unpack(mul2(A01, both(d))), e1 = unpack(mul2(A23, both(d)));
-      const f2 x = both(d * u[i]);
-      const f2 h0 = fma2(pack(ex2(e0.x), ex2(e0.y)), pack(s[i].x, s[i].y), mul2(x, pack(Bv[i][0], Bv[i][1])));
-      const f2 h1 = fma2(pack(ex2(e1.x), ex2(e1.y)), pack(s[i].z, s[i].w), mul2(x, pack(Bv[i][2], Bv[i][3])));
-      const float2 v0 = unpack(h0), v1 = unpack(h1);
-      *reinterpret_cast<float4 *>(S[i]) = make_float4(v0.x, v0.y, v1.x, v1.y);
-      const float2 w = unpack(fma2(h1, pack(Cv[i][2], Cv[i][3]), mul2(h0, pack(Cv[i][0], Cv[i][1]))));
-      float y = w.x + w.y;
+  for (int q = 0; q < 2; ++q) {
+    const f2 A0 = mul2(pack(A[q].x, A[q].y), both(kLog2e)), A1 = mul2(pack(A[q].z, A[q].w), both(kLog2e));
+    const float2 e0 = unpack(mul2(A0, step)), e1 = unpack(mul2(A1, step));
+    const f2 h0 = fma2(pack(ex2(e0.x), ex2(e0.y)), pack(s[q].x, s[q].y), mul2(xu, B[q].pair(0)));
+    const f2 h1 = fma2(pack(ex2(e1.x), ex2(e1.y)), pack(s[q].z, s[q].w), mul2(xu, B[q].pair(1)));
+    sum = q ? fma2(h0, C[q].pair(0), sum) : mul2(h0, C[q].pair(0));
+    sum = fma2(h1, C[q].pair(1), sum);
+    __stcs(reinterpret_cast<ulonglong2 *>(S + q * (N / 2)), ulonglong2{h0, h1});
+  }
+  const float2 w = unpack(sum);
+  float y = w.x + w.y;
+  const unsigned group = (unsigned)((1ull << L) - 1) << (threadIdx.x % 32 / L * L);
 #pragma unroll
-      for (int off = L / 2; off > 0; off >>= 1) y += __shfl_xor_sync(group, y, off);
-      if (lane == 0) {
-        y = fmaf(skip, u[i], y);
-        if (a.z.p) y *= silu(z[i]);
-        Io<TI>::st(static_cast<TI *>(a.y) + (long long)(r + i) * a.D + c, y);
-      }
-    }
+  for (int off = L / 2; off > 0; off >>= 1) y += __shfl_xor_sync(group, y, off);
+  if (lane == 0) {
+    y = fmaf(skip, u, y);
+    if (gated) y *= silu(z);
+    Io<TI>::st(static_cast<TI *>(a.y) + r * a.D + c, y);
   }
 }
 
@@ -599,13 +611,11 @@ kda_status launch_scan(const ScanArgs &a, const ScanPlan &p, int cut, cudaStream
 }
 template <typename TI, int N>
 kda_status launch_step(StepArgs a, cudaStream_t st) {
-  constexpr int kChans = kStepThreads / (N / kPer);
+  constexpr int kChans = kStepThreads / (N / 8);
   a.cblocks = (unsigned)(((long long)a.D + kChans - 1) / kChans);
-  const auto blocks = [&] { return (long long)a.cblocks * ((a.R + a.rows - 1) / a.rows); };
-  a.rows = 4;  // fewer where that would leave SMs without four CTAs
-  while (a.rows > 1 && blocks() < 152 * 4) a.rows /= 2;
-  if (blocks() > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  selective_step_kernel<TI, N><<<(unsigned)blocks(), kStepThreads, 0, st>>>(a);
+  const long long blocks = (long long)a.cblocks * a.R;
+  if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  selective_step_kernel<TI, N><<<(unsigned)blocks, kStepThreads, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -728,7 +738,12 @@ extern "C" kda_status kda_selective_step(const void *u, const void *delta, const
   const StepArgs a{{u, strides[0], 0}, {delta, strides[1], 0}, {Bm, strides[2], 0},
                    {Cm, strides[3], 0}, {z, z ? strides[4] : 0, 0},
                    A, Dskip, delta_bias, S, slots, n_slots, y, R, D, G,
-                   (flags & KDA_SCAN_SOFTPLUS) != 0u, 0, 0};
+                   (flags & KDA_SCAN_SOFTPLUS) != 0u,
+                   ((reinterpret_cast<uintptr_t>(Bm) | (uintptr_t)(strides[2] * e)) % (4 * e) == 0
+                        ? kVecB : 0) |
+                       ((reinterpret_cast<uintptr_t>(Cm) | (uintptr_t)(strides[3] * e)) % (4 * e) == 0
+                            ? kVecC : 0),
+                   0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_step_n<__nv_bfloat16>(a, N, st) : launch_step_n<float>(a, N, st);
 }

@@ -343,8 +343,8 @@ template <typename TI, int V> kda_status launch_conv_step(ConvStepArgs a, int W,
     const long long per = (long long)a.rows * (kConvThreads / a.cx);
     return a.cblocks * ((a.N + per - 1) / per);
   };
-  a.rows = 4;  // fewer where that would leave SMs without four CTAs
-  while (a.rows > 1 && blocks() < 152 * 4) a.rows /= 2;
+  a.rows = 4;  // fewer where that would leave SMs without two CTAs
+  while (a.rows > 1 && blocks() < 152 * 2) a.rows /= 2;
   const long long n = blocks();
   if (n > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
   const unsigned g = (unsigned)n;
