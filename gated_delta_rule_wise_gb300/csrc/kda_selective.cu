@@ -37,15 +37,15 @@ struct ScanArgs {
 
 constexpr int kMaxSplit = 64;      // parts of a sequence
 constexpr int kTargetWarps = 1216; // 152 SMs x 4 schedulers x 2
-constexpr unsigned kVecU = 1, kVecDelta = 2, kVecB = 4, kVecC = 8, kVecZ = 16;
+constexpr unsigned kVecU = 1, kVecDelta = 2, kVecB = 4, kVecC = 8, kVecZ = 16,
+                   kVecY = 32;
 
 struct ScanPlan {
   float *state;  // [split][B][D][N]: 0: h0; j: what part j - 1 leaves (0 from h0, others from 0)
   float *sum;    // [split][B][D]: sum of part j's step sizes
   int split, part;  // parts of a sequence, tokens of one
   int tiles_g;      // channel tiles of a group
-  unsigned vec;     // inputs that can be read two (u, delta, z) or four (B, C) values at a time
-  bool pairs;       // every row of y starts on two values
+  unsigned vec;     // tensors that can be read or written four (B, C: two) values at a time
 };
 
 // n (0, 1, 2) values from p on; `wide`: both in one load.  What is missing is zero.
@@ -79,6 +79,37 @@ __device__ __forceinline__ f2 softplus2(f2 x) {
   return fma2(s, e, pack(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
+// n (0 to 4) values from p on; `wide`: all or none of them, in one load.  What is
+// missing is zero.
+template <typename TI> struct Four {
+  typename Two<TI>::raw v[2];
+  __device__ __forceinline__ void load(const TI *p, int n, bool wide) {
+    if (wide) {
+      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
+      four w{};
+      if (n > 0) w = *reinterpret_cast<const four *>(p);
+      v[0] = w.x, v[1] = w.y;
+    } else {
+      v[0] = load_two<TI>(p, n, false), v[1] = load_two<TI>(p + 2, n - 2, false);
+    }
+  }
+  __device__ __forceinline__ f2 pair(int i) const { return Two<TI>::widen(v[i]); }
+  __device__ __forceinline__ void narrow(int i, f2 x) { v[i] = Two<TI>::narrow(x); }
+  // the first n of them to p, `wide`: all in one store
+  __device__ __forceinline__ void store(TI *p, int n, bool wide) const {
+    if (wide) {
+      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
+      *reinterpret_cast<four *>(p) = four{v[0], v[1]};
+    } else {
+      const float2 a = unpack(pair(0)), b = unpack(pair(1));
+      if (n > 0) Io<TI>::st(p, a.x);
+      if (n > 1) Io<TI>::st(p + 1, a.y);
+      if (n > 2) Io<TI>::st(p + 2, b.x);
+      if (n > 3) Io<TI>::st(p + 3, b.y);
+    }
+  }
+};
+
 // How a CTA is cut: REC recurrence threads, each with PER entries of CH channels;
 // IO threads that prepare operands and as many that write y.
 template <int CH_, int PER_, int REC_, int IO_> struct Cut {
@@ -89,8 +120,13 @@ template <int N, class X, bool kOut> struct ScanShape {
   static constexpr int CT = X::REC / L * X::CH;    // channels of a CTA
   static constexpr int TT = CT >= 128 ? 8 : CT >= 64 ? 16 : 32;  // tokens of a tile
   static constexpr int kThreads = X::REC + (kOut ? 2 : 1) * X::IO;
-  static constexpr int kDx = 2 * TT * CT * 8;  // (dt, dt u), two tiles
-  static constexpr int kBC = (kOut ? 4 : 2) * TT * N * 4;
+  // What the recurrence reads is in pairs of tokens, so that its packed products run over two
+  // tokens: (dt0, dt1, dt0 u0, dt1 u1) of a channel.  A pair's channels lie in four planes by
+  // their last two bits, 32 bytes apart in the banks: free of conflicts for the threads that
+  // write four channels as for the lanes that read neighbouring ones.
+  static constexpr int kPlane = CT * 4 + 32, kPairRow = 4 * kPlane;
+  static constexpr int kDx = 2 * (TT / 2) * kPairRow;
+  static constexpr int kBC = (kOut ? 4 : 2) * TT * N * 4;  // [pair][n](token 0, token 1)
   static constexpr int kY = kOut ? 2 * TT * CT * 4 : 0;
   static constexpr int kSmem = kDx + kBC + kY;
 };
@@ -163,7 +199,8 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     // ---- recurrence: L lanes of PER entries share CH channels
     const int ch = tid / L * CH, lane = tid % L, n0 = lane * PER;
     const long long plane = (long long)a.B * a.D * N;
-    f2 A2[CH][PER / 2], h[CH][PER / 2];
+    f2 A2[CH][PER];  // both halves A log2 e
+    float h[CH][PER];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const bool live = ch + j < chans;
@@ -189,49 +226,40 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
             s.z = fmaf(ex2(sum * v.z), s.z, e.z), s.w = fmaf(ex2(sum * v.w), s.w, e.w);
           }
         }
-        A2[j][2 * i] = pack(v.x, v.y), A2[j][2 * i + 1] = pack(v.z, v.w);
-        h[j][2 * i] = pack(s.x, s.y), h[j][2 * i + 1] = pack(s.z, s.w);
+        A2[j][4 * i] = both(v.x), A2[j][4 * i + 1] = both(v.y);
+        A2[j][4 * i + 2] = both(v.z), A2[j][4 * i + 3] = both(v.w);
+        h[j][4 * i] = s.x, h[j][4 * i + 1] = s.y, h[j][4 * i + 2] = s.z, h[j][4 * i + 3] = s.w;
       }
     }
-    // Blocks of TB tokens give the four sums (token, channel) that lane_sums takes; the next
-    // block's operands are fetched before this one's sums are stored, which loads may not pass.
-    constexpr int TB = 4 / CH;
-    struct Block {
-      float2 d[TB][CH];
-      ulonglong2 B[TB][PER / 4], C[TB][PER / 4];
+    // A block is two items of one channel and two tokens: two pairs of tokens (CH = 1) or two
+    // channels (CH = 2).  It gives the four values (token i / CH, channel i % CH) that LaneSums
+    // takes.  A pair's operands are fetched while the one before is in work.
+    struct Pair {
+      ulonglong2 d[CH], B[PER / 2], C[PER / 2];
     };
+    constexpr int TB = 4 / CH;
     float sum[CH] = {};
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
-      const char *q = dx + ((k & 1) * TT * CT + ch) * 8;
-      const char *Bk = bc + ((k & 1) * TT * N + n0) * 4;
-      // value i of a block: token i / CH, channel i % CH; a lane stores kOwn of them
+      const char *q = dx + (k & 1) * (TT / 2) * S::kPairRow + ch % 4 * S::kPlane + ch / 4 * 16;
+      const char *Bk = bc + ((k & 1) * TT * N + 2 * n0) * 4;
+      // a lane stores kOwn values of a block
       constexpr int kOwn = L >= 4 ? 1 : 4 / L;
       float *yk = ys + (k & 1) * TT * CT + ch + lane % 4 * kOwn / CH * CT + lane % 4 * kOwn % CH;
-      const auto fetch = [&](Block &x, int t) {
+      const auto fetch = [&](Pair &x, int t) {
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-          if (CH == 1) {
-            x.d[i][0] = *reinterpret_cast<const float2 *>(q + (t + i) * CT * 8);
-          } else {
+        for (int j = 0; j < CH; ++j)
+          x.d[j] = *reinterpret_cast<const ulonglong2 *>(q + t / 2 * S::kPairRow + j * S::kPlane);
 #pragma unroll
-            for (int j = 0; j < CH; j += 2) {
-              const float4 v = *reinterpret_cast<const float4 *>(q + (t + i) * CT * 8 + j * 8);
-              x.d[i][j] = make_float2(v.x, v.y);
-              x.d[i][j + 1] = make_float2(v.z, v.w);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < PER / 4; ++j) {
-            x.B[i][j] = *reinterpret_cast<const ulonglong2 *>(Bk + (t + i) * N * 4 + j * 16);
-            if (kOut)
-              x.C[i][j] = *reinterpret_cast<const ulonglong2 *>(Bk + (2 * TT + t + i) * N * 4 + j * 16);
-          }
+        for (int n = 0; n < PER / 2; ++n) {
+          x.B[n] = *reinterpret_cast<const ulonglong2 *>(Bk + t * N * 4 + n * 16);
+          if (kOut)
+            x.C[n] = *reinterpret_cast<const ulonglong2 *>(Bk + (2 * TT + t) * N * 4 + n * 16);
         }
       };
       float tile_sum[CH] = {};
-      // The sums over lanes of the block before run between this one's products:
-      // each exchange has a quarter of a block to come back.
+      // The sums over lanes of the block before run between this one's products: each
+      // exchange has a quarter of a block to come back.
       LaneSums<L> sums{};
       const auto store = [&](int t) {
         if (L <= 4 || lane < 4) {
@@ -239,48 +267,47 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
           for (int i = 0; i < kOwn; ++i) yk[(t + i / CH) * CT + i % CH] = sums.v[i];
         }
       };
-      const auto work = [&](const Block &x, int t) {
-        float y[4];
+      const auto item = [&](const Pair &x, int j, int which) {
+        f2 s = 0;
 #pragma unroll
-        for (int i = 0; i < TB; ++i) {
-#pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            if (kOut) sums.step(i * CH + j, lane);
-            const f2 dt = both(x.d[i][j].x), xu = both(x.d[i][j].y);
-            f2 s;
-#pragma unroll
-            for (int n = 0; n < PER / 2; ++n) {
-              const ulonglong2 Bn = x.B[i][n / 2], Cn = x.C[i][n / 2];
-              const float2 e = unpack(mul2(A2[j][n], dt));
-              h[j][n] = fma2(pack(ex2(e.x), ex2(e.y)), h[j][n], mul2(xu, n % 2 ? Bn.y : Bn.x));
-              if (kOut) {
-                const f2 c = n % 2 ? Cn.y : Cn.x;
-                s = n ? fma2(h[j][n], c, s) : mul2(h[j][n], c);
-              }
-            }
-            if (kOut) {
-              const float2 w = unpack(s);
-              y[i * CH + j] = w.x + w.y;
-            } else {
-              tile_sum[j] += x.d[i][j].x;
-            }
+        for (int n = 0; n < PER; ++n) {
+          if (kOut && n % (PER / 2) == 0) sums.step(2 * which + n / (PER / 2), lane);
+          const ulonglong2 Bn = x.B[n / 2], Cn = x.C[n / 2];
+          const float2 e = unpack(mul2(A2[j][n], x.d[j].x));
+          const float2 xb = unpack(mul2(x.d[j].y, n % 2 ? Bn.y : Bn.x));
+          const float h0 = fmaf(ex2(e.x), h[j][n], xb.x);
+          h[j][n] = fmaf(ex2(e.y), h0, xb.y);
+          if (kOut) {
+            const f2 hh = pack(h0, h[j][n]), c = n % 2 ? Cn.y : Cn.x;
+            s = n ? fma2(hh, c, s) : mul2(hh, c);
           }
         }
-        if (kOut) {
-          sums.step(4, lane);
-          if (t > 0) store(t - TB);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sums.v[i] = y[i];
+        if (!kOut) {
+          const float2 dt = unpack(x.d[j].x);
+          tile_sum[j] += dt.x + dt.y;
         }
+        return unpack(s);
       };
-      Block x0, x1;
+      const auto finish = [&](float2 a, float2 b, int t) {  // t: the block's first token
+        if (!kOut) return;
+        sums.step(4, lane);
+        if (t > 0) store(t - TB);
+        sums.v[0] = a.x, sums.v[3] = b.y;
+        sums.v[CH == 1 ? 1 : 2] = a.y, sums.v[CH == 1 ? 2 : 1] = b.x;
+      };
+      Pair x0, x1;
       fetch(x0, 0);
-#pragma unroll 1
-      for (int t = 0; t < TT; t += 2 * TB) {
-        fetch(x1, t + TB);
-        work(x0, t);
-        fetch(x0, t + 2 * TB < TT ? t + 2 * TB : 0);
-        work(x1, t + TB);
+#pragma unroll
+      for (int t = 0; t < TT; t += 4) {
+        fetch(x1, t + 2);
+        const float2 y0 = item(x0, 0, 0);
+        if (CH == 2) finish(y0, item(x0, CH - 1, 1), t);
+        if (t + 4 < TT) fetch(x0, t + 4);
+        const float2 y1 = item(x1, 0, CH == 1);
+        if (CH == 2)
+          finish(y1, item(x1, CH - 1, 1), t + 2);
+        else
+          finish(y0, y1, t);
       }
       if (kOut) {
 #pragma unroll
@@ -299,106 +326,106 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       float *to = kOut ? (last ? a.hT : nullptr) : p.state + (part + 1) * plane;
 #pragma unroll
       for (int i = 0; i < PER / 4; ++i) {
-        const float2 s0 = unpack(h[j][2 * i]), s1 = unpack(h[j][2 * i + 1]);
-        if (to) *reinterpret_cast<float4 *>(to + so + 4 * i) = make_float4(s0.x, s0.y, s1.x, s1.y);
+        if (to)
+          *reinterpret_cast<float4 *>(to + so + 4 * i) =
+              make_float4(h[j][4 * i], h[j][4 * i + 1], h[j][4 * i + 2], h[j][4 * i + 3]);
       }
       if (!kOut && n0 == 0) p.sum[((long long)part * a.B + b) * a.D + c] = sum[j];
     }
     return;
   }
 
-  // This thread's two channels, its first token of a tile and the step to its next.
-  constexpr int kRows = kIo / (CT / 2), kTimes = (TT + kRows - 1) / kRows;
+  // This thread's four channels and its pair of tokens.
+  static_assert(CT / 4 * (TT / 2) <= kIo, "a pair of tokens per thread");
   const int io = (tid - kRec) % kIo;
-  const int ch = io % (CT / 2) * 2, tr = io / (CT / 2);
-  const int two = min(max(chans - ch, 0), 2);
-  const auto per_channel = [&](const float *q) {
-    return q ? pack(two > 0 ? q[c0 + ch] : 0.f, two > 1 ? q[c0 + ch + 1] : 0.f) : 0;
+  const int ch = io % (CT / 4) * 4, pr = io / (CT / 4);
+  const int four = pr < TT / 2 ? min(max(chans - ch, 0), 4) : 0;
+  const auto per_channel = [&](const float *q, int i) {
+    return q ? pack(four > i ? q[c0 + ch + i] : 0.f, four > i + 1 ? q[c0 + ch + i + 1] : 0.f) : 0;
   };
-  typedef typename Two<TI>::raw raw2;
-  // Two channels of the thread's tokens; q is the first one's place in the tile.
-  const auto rows_of = [&](raw2 (&v)[kTimes], const TI *q, long long step, int rows, bool wide) {
-    if (wide && rows >= TT && two == 2 && kRows * kTimes == TT) {
-#pragma unroll
-      for (int i = 0; i < kTimes; ++i) v[i] = *reinterpret_cast<const raw2 *>(q + i * step);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTimes; ++i) {
-        const int t = tr + i * kRows;
-        v[i] = load_two<TI>(q + i * step, t < rows && t < TT ? two : 0, wide);
-      }
-    }
+  // The four channels of the thread's tokens, `rows` tokens before the end.
+  const auto rows_of = [&](Four<TI> (&v)[2], const TI *q, long long st, int rows, bool wide) {
+    v[0].load(q, 2 * pr < rows ? four : 0, wide);
+    v[1].load(q + st, 2 * pr + 1 < rows ? four : 0, wide);
   };
   const auto place = [&](const Rows &x) {
-    return static_cast<const TI *>(x.p) + b * x.sb + c0 + ch + (t0 + tr) * x.st;
+    return static_cast<const TI *>(x.p) + b * x.sb + c0 + ch + (t0 + 2 * pr) * x.st;
   };
   const TI *u = place(a.u);
-  const long long u_step = kRows * a.u.st, u_tile = TT * a.u.st;
+  Four<TI> ru[2];
 
   if (tid < kRec + kIo) {
     // ---- step sizes, B and C of the next tile, read one tile further ahead
     const TI *de = place(a.delta);
-    const long long d_step = kRows * a.delta.st, d_tile = TT * a.delta.st;
-    // four values of B and C: token io / (N / 4) of a tile, and kIo / (N / 4) tokens on
-    const int qt = io / (N / 4);
+    Four<TI> rd[2];
+    // two values of B and C of two tokens: pair io / (N / 2) of a tile, kIo / (N / 2) pairs on
+    constexpr int kItems = TT / 2 * (N / 2), kQ = kItems > kIo ? kItems / kIo : 1;
+    static_assert(kItems <= kIo || kItems % kIo == 0, "whole rounds");
+    const int qp = io / (N / 2), qn = io % (N / 2) * 2;
+    const bool has_item = qp < TT / 2;
     const auto group = [&](const Rows &x) {
-      return static_cast<const TI *>(x.p) + b * x.sb + (long long)g * N + io % (N / 4) * 4 +
-             (t0 + qt) * x.st;
+      return static_cast<const TI *>(x.p) + b * x.sb + (long long)g * N + qn +
+             (t0 + 2 * qp) * x.st;
     };
     const TI *Bm = group(a.Bm), *Cm = group(a.Cm);
-    constexpr int kQuads = TT * N / 4 / kIo;  // groups of four values of B, and of C
-    static_assert(kQuads * kIo * 4 == TT * N || TT * N / 4 < kIo, "whole rounds");
-    constexpr int kQ = kQuads > 0 ? kQuads : 1;
-    const bool has_quad = TT * N / 4 >= kIo || io < TT * N / 4;
-    raw2 ru[kTimes], rd[kTimes], rB[kQ][2], rC[kQ][2];
-    const f2 bias = per_channel(a.bias);
-    const auto quad = [&](raw2 (&v)[2], const TI *q, int t, int rows, bool wide) {
-      const bool in = has_quad && t < rows;
-      if (wide) {
-        typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
-        four w{};
-        if (in) w = *reinterpret_cast<const four *>(q);
-        v[0] = w.x, v[1] = w.y;
-      } else {
-        v[0] = load_two<TI>(q, in ? 2 : 0, false), v[1] = load_two<TI>(q + 2, in ? 2 : 0, false);
-      }
+    typename Two<TI>::raw rB[kQ][2], rC[kQ][2];
+    const f2 bias[2] = {per_channel(a.bias, 0), per_channel(a.bias, 2)};
+    const auto item = [&](typename Two<TI>::raw (&v)[2], const TI *q, long long st, int t, int rows,
+                          bool wide) {
+      v[0] = load_two<TI>(q, t < rows ? 2 : 0, wide);
+      v[1] = load_two<TI>(q + st, t + 1 < rows ? 2 : 0, wide);
     };
     int ahead = t1 - t0;  // tokens from the tile that is read next to the end
     const auto load = [&]() {
-      rows_of(ru, u, u_step, ahead, p.vec & kVecU);
-      rows_of(rd, de, d_step, ahead, p.vec & kVecDelta);
+      rows_of(ru, u, a.u.st, ahead, p.vec & kVecU);
+      rows_of(rd, de, a.delta.st, ahead, p.vec & kVecDelta);
+      if (has_item) {
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        constexpr int kStep = kIo / (N / 4);
-        quad(rB[i], Bm + i * kStep * a.Bm.st, qt + i * kStep, ahead, p.vec & kVecB);
-        if (kOut) quad(rC[i], Cm + i * kStep * a.Cm.st, qt + i * kStep, ahead, p.vec & kVecC);
+        for (int i = 0; i < kQ; ++i) {
+          const int t = 2 * (qp + i * (kIo / (N / 2)));
+          const long long on = 2 * i * (kIo / (N / 2));
+          item(rB[i], Bm + on * a.Bm.st, a.Bm.st, t, ahead, p.vec & kVecB);
+          if (kOut) item(rC[i], Cm + on * a.Cm.st, a.Cm.st, t, ahead, p.vec & kVecC);
+        }
       }
-      u += u_tile, de += d_tile, Bm += TT * a.Bm.st, Cm += TT * a.Cm.st, ahead -= TT;
+      u += TT * a.u.st, de += TT * a.delta.st, Bm += TT * a.Bm.st, Cm += TT * a.Cm.st, ahead -= TT;
     };
     // A token behind the end gets step 0 and B = 0: decay 1, nothing added.
     const auto prepare = [&](int k) {
-      char *q = dx + ((k & 1) * TT * CT + ch) * 8;
       const int rows = t1 - t0 - k * TT;
+      if (pr < TT / 2) {
+        char *row = dx + ((k & 1) * (TT / 2) + pr) * S::kPairRow + ch / 4 * 16;
+        f2 d[2][2];  // [token][channels 0 and 1, 2 and 3]
 #pragma unroll
-      for (int i = 0; i < kTimes; ++i) {
-        const int t = tr + i * kRows;
-        f2 dt = add2(Two<TI>::widen(rd[i]), bias);
-        if (a.softplus) dt = softplus2(dt);
-        if (t >= rows) dt = 0;
-        const float2 d = unpack(dt), v = unpack(mul2(dt, Two<TI>::widen(ru[i])));
-        if (kRows * kTimes == TT || t < TT)
-          *reinterpret_cast<float4 *>(q + t * CT * 8) = make_float4(d.x, v.x, d.y, v.y);
+        for (int e = 0; e < 4; ++e) {
+          f2 dt = add2(rd[e / 2].pair(e % 2), bias[e % 2]);
+          if (a.softplus) dt = softplus2(dt);
+          d[e / 2][e % 2] = dt;
+        }
+        if (rows < TT) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (2 * pr + e >= rows) d[e][0] = d[e][1] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 d0 = unpack(d[0][i]), d1 = unpack(d[1][i]);
+          const float2 x0 = unpack(mul2(d[0][i], ru[0].pair(i))), x1 = unpack(mul2(d[1][i], ru[1].pair(i)));
+          *reinterpret_cast<float4 *>(row + 2 * i * S::kPlane) = make_float4(d0.x, d1.x, x0.x, x1.x);
+          *reinterpret_cast<float4 *>(row + (2 * i + 1) * S::kPlane) = make_float4(d0.y, d1.y, x0.y, x1.y);
+        }
       }
-      float *fb = reinterpret_cast<float *>(bc) + (k & 1) * TT * N;
+      if (has_item) {
+        float *fb = reinterpret_cast<float *>(bc) + (k & 1) * TT * N + qp * 2 * N + 2 * qn;
+        const auto put = [&](float *to, const typename Two<TI>::raw (&v)[2]) {
+          const float2 lo = unpack(Two<TI>::widen(v[0])), hi = unpack(Two<TI>::widen(v[1]));
+          *reinterpret_cast<float4 *>(to) = make_float4(lo.x, hi.x, lo.y, hi.y);
+        };
 #pragma unroll
-      for (int i = 0; i < kQ; ++i) {
-        if (!has_quad) continue;
-        const int e = (io + i * kIo) * 4;
-        *reinterpret_cast<ulonglong2 *>(fb + e) =
-            ulonglong2{Two<TI>::widen(rB[i][0]), Two<TI>::widen(rB[i][1])};
-        if (kOut)
-          *reinterpret_cast<ulonglong2 *>(fb + 2 * TT * N + e) =
-              ulonglong2{Two<TI>::widen(rC[i][0]), Two<TI>::widen(rC[i][1])};
+        for (int i = 0; i < kQ; ++i) {
+          put(fb + i * (kIo / (N / 2)) * 2 * N, rB[i]);
+          if (kOut) put(fb + 2 * TT * N + i * (kIo / (N / 2)) * 2 * N, rC[i]);
+        }
       }
     };
     if (tiles > 0) {
@@ -421,49 +448,40 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
   // ---- y of the tile before: D u, the gate, rounding
   const bool gated = a.z.p != nullptr;
   const TI *z = place(a.z);
-  const long long z_step = kRows * a.z.st, z_tile = TT * a.z.st;
-  const f2 skip = per_channel(a.Dskip);
-  TI *y = static_cast<TI *>(a.y) + ((long long)b * a.T + t0 + tr) * a.D + c0 + ch;
-  const long long y_step = (long long)kRows * a.D, y_tile = (long long)TT * a.D;
-  raw2 ru[kTimes], rz[kTimes];
+  Four<TI> rz[2];
+  const f2 skip[2] = {per_channel(a.Dskip, 0), per_channel(a.Dskip, 2)};
+  TI *y = static_cast<TI *>(a.y) + ((long long)b * a.T + t0 + 2 * pr) * a.D + c0 + ch;
   int rows = t1 - t0;  // tokens from the tile in work to the end
-  const auto load = [&](int left) {
-    rows_of(ru, u, u_step, left, p.vec & kVecU);
-    if (gated) rows_of(rz, z, z_step, left, p.vec & kVecZ);
-    u += u_tile, z += z_tile;
+  const auto load = [&]() {
+    rows_of(ru, u, a.u.st, rows, p.vec & kVecU);
+    if (gated) rows_of(rz, z, a.z.st, rows, p.vec & kVecZ);
+    u += TT * a.u.st, z += TT * a.z.st;
   };
   const auto write = [&](int k) {
-    const float *sy = ys + (k & 1) * TT * CT + tr * CT + ch;
-    f2 v[kTimes];
+    if (four > 0) {
+      const float *sy = ys + ((k & 1) * TT + 2 * pr) * CT + ch;
 #pragma unroll
-    for (int i = 0; i < kTimes; ++i) {
-      if (kRows * kTimes != TT && tr >= TT) break;
-      v[i] = fma2(skip, Two<TI>::widen(ru[i]), *reinterpret_cast<const f2 *>(sy + i * kRows * CT));
-      if (gated) v[i] = mul2(v[i], silu2(Two<TI>::widen(rz[i])));
-    }
-    if (p.pairs && rows >= TT && two == 2 && kRows * kTimes == TT) {
+      for (int e = 0; e < 2; ++e) {
+        const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(sy + e * CT);
+        Four<TI> o;
 #pragma unroll
-      for (int i = 0; i < kTimes; ++i)
-        *reinterpret_cast<raw2 *>(y + i * y_step) = Two<TI>::narrow(v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTimes; ++i) {
-        const int t = tr + i * kRows;
-        if (t >= rows || t >= TT) break;
-        const float2 w = unpack(v[i]);
-        if (two > 0) Io<TI>::st(y + i * y_step, w.x);
-        if (two > 1) Io<TI>::st(y + i * y_step + 1, w.y);
+        for (int i = 0; i < 2; ++i) {
+          f2 v = fma2(skip[i], ru[e].pair(i), i ? s.y : s.x);
+          if (gated) v = mul2(v, silu2(rz[e].pair(i)));
+          o.narrow(i, v);
+        }
+        if (2 * pr + e < rows) o.store(y + (long long)e * a.D, four, p.vec & kVecY);
       }
     }
-    y += y_tile, rows -= TT;
+    y += (long long)TT * a.D, rows -= TT;
   };
-  if (tiles > 0) load(rows);
+  if (tiles > 0) load();
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < tiles; ++k) {
     if (k > 0) {
       write(k - 1);
-      load(rows);
+      load();
     }
     __syncthreads();
   }
@@ -478,23 +496,8 @@ struct StepArgs {
   int n_slots;
   void *y;
   int R, D, G, softplus;
-  unsigned vec;  // of B and C, as in ScanPlan
+  unsigned vec;  // whether B and C can be read four values at a time
   unsigned cblocks;
-};
-
-// Four values of B or C from p on, in one load where they are aligned.
-template <typename TI> struct Four {
-  typename Two<TI>::raw v[2];
-  __device__ __forceinline__ void load(const TI *p, bool wide) {
-    if (wide) {
-      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
-      const four w = *reinterpret_cast<const four *>(p);
-      v[0] = w.x, v[1] = w.y;
-    } else {
-      v[0] = load_two<TI>(p, 2, false), v[1] = load_two<TI>(p + 2, 2, false);
-    }
-  }
-  __device__ __forceinline__ f2 pair(int i) const { return Two<TI>::widen(v[i]); }
 };
 
 // A group of N / 8 lanes takes one channel of one row; a lane's entries are the
@@ -530,8 +533,8 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
   const float z = gated ? Io<TI>::ld(static_cast<const TI *>(a.z.p) + r * a.z.sb + c) : 0.f;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    B[q].load(pB + q * (N / 2), a.vec & kVecB);
-    C[q].load(pC + q * (N / 2), a.vec & kVecC);
+    B[q].load(pB + q * (N / 2), 4, a.vec & kVecB);
+    C[q].load(pC + q * (N / 2), 4, a.vec & kVecC);
     A[q] = *reinterpret_cast<const float4 *>(a.A + e + q * (N / 2));
   }
   const float skip = a.Dskip ? a.Dskip[c] : 0.f;
@@ -565,15 +568,16 @@ struct ScanChoice {
   int cut, split;  // which Cut, parts of a sequence
 };
 // Two channels per lane group halve the reads of B and C per entry, and the warps: worth it
-// once the state alone fills the schedulers (8192 channels of 16 entries: 129 against 133 us
-// for 2048 tokens; 4096 channels: 990 against 590 us for 16384).  Where one channel per group
-// leaves most of them empty, the tokens are split as well, at the price of the exponentials
-// of a second pass: 1536 channels, 8192 tokens: 6 parts 146 us, one 305 us; 4096 channels:
-// 4 parts 746 us, one 590 us, so two parts never pay.
+// once there are warps for two CTAs on every SM all the same (16384 channels of 16 entries,
+// 2048 tokens: 193 against 236 us; 8192 channels: 131 against 121; 4096 channels, 16384
+// tokens: 988 against 524).  Where one channel per group leaves most schedulers empty, the
+// tokens are split as well, at the price of the exponentials of a second pass: 1536 channels,
+// 8192 tokens: 6 parts 130 us, one 271 us; 4096 channels, 16384 tokens: 4 parts 703 us, one
+// 524 us, so two parts never pay.
 ScanChoice scan_choice(int B, int T, int D, int N) {
   const long long warps = ((long long)B * D * N + 127) / 128;  // with four entries per thread
   ScanChoice c;
-  c.cut = warps >= kTargetWarps * 4 / 5 ? 2 : 1;
+  c.cut = warps > kTargetWarps ? 2 : 1;
   long long s = warps > 0 ? kTargetWarps / warps : 1;
   if (s > T / 64) s = T / 64;
   if (s > kMaxSplit) s = kMaxSplit;
@@ -697,20 +701,19 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
   p.split = choice.split;
   // a part is whole tiles, so its tokens need no masks but at the sequence's end
   p.part = (T + p.split * 32 - 1) / (p.split * 32) * 32;
-  p.pairs = D % 2 == 0 && D / G % 2 == 0;
   p.tiles_g = 0;  // by the kernel's shape
   p.state = static_cast<float *>(workspace);
   p.sum = p.state + (size_t)p.split * B * D * N;
-  // wide reads: the address and both strides are multiples of n values, and
-  // no row of a group ends inside a pair
+  // wide accesses: the address and both strides are multiples of n values, and no row of a
+  // group ends inside four channels
   const auto wide = [&](const void *q, int i, int n) {
     return (reinterpret_cast<uintptr_t>(q) | (uintptr_t)(strides[i] * e) |
             (uintptr_t)(strides[i + 1] * e)) % (n * e) == 0;
   };
-  p.vec = (wide(Bm, 4, 4) ? kVecB : 0) | (wide(Cm, 6, 4) ? kVecC : 0);
-  if (D / G % 2 == 0)
-    p.vec |= (wide(u, 0, 2) ? kVecU : 0) | (wide(delta, 2, 2) ? kVecDelta : 0) |
-             (z && wide(z, 8, 2) ? kVecZ : 0);
+  p.vec = (wide(Bm, 4, 2) ? kVecB : 0) | (wide(Cm, 6, 2) ? kVecC : 0);
+  if (D / G % 4 == 0)
+    p.vec |= (wide(u, 0, 4) ? kVecU : 0) | (wide(delta, 2, 4) ? kVecDelta : 0) |
+             (z && wide(z, 8, 4) ? kVecZ : 0) | kVecY;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.cut, N, st)
                         : launch_scan_n<float>(a, p, choice.cut, N, st);
