@@ -68,6 +68,10 @@ template <> struct Two<__nv_bfloat16> {
   static __device__ __forceinline__ f2 widen(raw v) {
     return pack(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
   }
+  // the first values of a and b, and their second ones
+  static __device__ __forceinline__ void trade(raw a, raw b, raw &first, raw &second) {
+    first = __byte_perm(a, b, 0x5410), second = __byte_perm(a, b, 0x7632);
+  }
   static __device__ __forceinline__ raw narrow(f2 v) {
     const float2 x = unpack(v);
     const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
@@ -78,6 +82,10 @@ template <> struct Two<float> {
   typedef f2 raw;
   static __device__ __forceinline__ raw join(float lo, float hi) { return pack(lo, hi); }
   static __device__ __forceinline__ f2 widen(raw v) { return v; }
+  static __device__ __forceinline__ void trade(raw a, raw b, raw &first, raw &second) {
+    const float2 x = unpack(a), y = unpack(b);
+    first = pack(x.x, y.x), second = pack(x.y, y.y);
+  }
   static __device__ __forceinline__ raw narrow(f2 v) { return v; }
 };
 

@@ -35,17 +35,19 @@ struct ScanArgs {
 
 // ---------------------------------------------------------------- prompts
 
+constexpr int kRec = 128;          // recurrence threads of a CTA, kPer entries per channel each
+constexpr int kIo = 128;           // threads that prepare operands, and as many that write y
+constexpr int kPer = 4;
 constexpr int kMaxSplit = 64;      // parts of a sequence
 constexpr int kTargetWarps = 1216; // 152 SMs x 4 schedulers x 2
-constexpr unsigned kVecU = 1, kVecDelta = 2, kVecB = 4, kVecC = 8, kVecZ = 16,
-                   kVecY = 32;
 
 struct ScanPlan {
   float *state;  // [split][B][D][N]: 0: h0; j: what part j - 1 leaves (0 from h0, others from 0)
   float *sum;    // [split][B][D]: sum of part j's step sizes
   int split, part;  // parts of a sequence, tokens of one
   int tiles_g;      // channel tiles of a group
-  unsigned vec;     // tensors that can be read or written four (B, C: two) values at a time
+  // how many values of a row can be read or written at once: 4, 2 or 1
+  int u_at_once, delta_at_once, z_at_once, y_at_once, B_at_once, C_at_once;
 };
 
 // n (0, 1, 2) values from p on; `wide`: both in one load.  What is missing is zero.
@@ -54,14 +56,20 @@ __device__ __forceinline__ typename Two<TI>::raw load_two(const TI *p, int n, bo
   if (wide) return n > 0 ? *reinterpret_cast<const typename Two<TI>::raw *>(p) : 0;
   return Two<TI>::join(n > 0 ? p[0] : TI(0.f), n > 1 ? p[1] : TI(0.f));
 }
+__device__ __forceinline__ float relu(float x) {  // NaN stays NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+  return r;
+}
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  The argument's
 // rounding is put back into e (its residual is exact in one fma).  log1p(e) / e
 // is a polynomial of degree 9, the least relative maximum error on [0, 1]
 // (4.7e-9, found by reweighted least squares on Chebyshev points); in float32
 // its values are within 2.6 2^-24 relative, so small steps keep their precision.
+// |x| ends at 104, where e is 0 already: -inf gives 0, inf itself, NaN NaN.
 __device__ __forceinline__ f2 softplus2(f2 x) {
   const float2 v = unpack(x);
-  const f2 m = pack(-fabsf(v.x), -fabsf(v.y));
+  const f2 m = pack(-fminf(fabsf(v.x), 104.f), -fminf(fabsf(v.y), 104.f));
   const f2 t = mul2(m, both(kLog2e));
   const float2 tt = unpack(t);
   const f2 r = fma2(m, both(kLog2e), pack(-tt.x, -tt.y));
@@ -76,30 +84,31 @@ __device__ __forceinline__ f2 softplus2(f2 x) {
   s = fma2(s, e, both(3.332996368e-01f));
   s = fma2(s, e, both(-4.999990165e-01f));
   s = fma2(s, e, both(1.f));
-  return fma2(s, e, pack(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+  return fma2(s, e, pack(relu(v.x), relu(v.y)));
 }
 
-// n (0 to 4) values from p on; `wide`: all or none of them, in one load.  What is
-// missing is zero.
+// n (0 to 4) values from p on, `at_once` (4, 2 or 1) in a load or store; n is then a multiple
+// of it.  What is missing is zero.
 template <typename TI> struct Four {
+  typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type all;
   typename Two<TI>::raw v[2];
-  __device__ __forceinline__ void load(const TI *p, int n, bool wide) {
-    if (wide) {
-      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
-      four w{};
-      if (n > 0) w = *reinterpret_cast<const four *>(p);
+  __device__ __forceinline__ void load(const TI *p, int n, int at_once) {
+    if (at_once == 4) {
+      all w{};
+      if (n > 0) w = *reinterpret_cast<const all *>(p);
       v[0] = w.x, v[1] = w.y;
     } else {
-      v[0] = load_two<TI>(p, n, false), v[1] = load_two<TI>(p + 2, n - 2, false);
+      v[0] = load_two<TI>(p, n, at_once == 2), v[1] = load_two<TI>(p + 2, n - 2, at_once == 2);
     }
   }
   __device__ __forceinline__ f2 pair(int i) const { return Two<TI>::widen(v[i]); }
   __device__ __forceinline__ void narrow(int i, f2 x) { v[i] = Two<TI>::narrow(x); }
-  // the first n of them to p, `wide`: all in one store
-  __device__ __forceinline__ void store(TI *p, int n, bool wide) const {
-    if (wide) {
-      typedef typename std::conditional<sizeof(TI) == 2, uint2, ulonglong2>::type four;
-      *reinterpret_cast<four *>(p) = four{v[0], v[1]};
+  __device__ __forceinline__ void store(TI *p, int n, int at_once) const {
+    if (at_once == 4) {
+      if (n > 0) *reinterpret_cast<all *>(p) = all{v[0], v[1]};
+    } else if (at_once == 2) {
+      if (n > 0) *reinterpret_cast<typename Two<TI>::raw *>(p) = v[0];
+      if (n > 2) *reinterpret_cast<typename Two<TI>::raw *>(p + 2) = v[1];
     } else {
       const float2 a = unpack(pair(0)), b = unpack(pair(1));
       if (n > 0) Io<TI>::st(p, a.x);
@@ -110,23 +119,23 @@ template <typename TI> struct Four {
   }
 };
 
-// How a CTA is cut: REC recurrence threads, each with PER entries of CH channels;
-// IO threads that prepare operands and as many that write y.
-template <int CH_, int PER_, int REC_, int IO_> struct Cut {
-  static constexpr int CH = CH_, PER = PER_, REC = REC_, IO = IO_;
-};
-template <int N, class X, bool kOut> struct ScanShape {
-  static constexpr int L = N / X::PER;             // lanes that share a group of CH channels
-  static constexpr int CT = X::REC / L * X::CH;    // channels of a CTA
+template <typename TI, int N, int CH, bool kOut> struct ScanShape {
+  static constexpr int L = N / kPer;               // lanes that share a group of CH channels
+  static constexpr int CT = kRec / L * CH;         // channels of a CTA
   static constexpr int TT = CT >= 128 ? 8 : CT >= 64 ? 16 : 32;  // tokens of a tile
-  static constexpr int kThreads = X::REC + (kOut ? 2 : 1) * X::IO;
+  static constexpr int kThreads = kRec + (kOut ? 2 : 1) * kIo;
   // What the recurrence reads is in pairs of tokens, so that its packed products run over two
   // tokens: (dt0, dt1, dt0 u0, dt1 u1) of a channel.  A pair's channels lie in four planes by
   // their last two bits, 32 bytes apart in the banks: free of conflicts for the threads that
   // write four channels as for the lanes that read neighbouring ones.
   static constexpr int kPlane = CT * 4 + 32, kPairRow = 4 * kPlane;
   static constexpr int kDx = 2 * (TT / 2) * kPairRow;
-  static constexpr int kBC = (kOut ? 4 : 2) * TT * N * 4;  // [pair][n](token 0, token 1)
+  // B and C, [pair][n](token 0, token 1): with one channel per lane group as they are stored,
+  // since half the bytes leave shared memory then (8192 channels: 113 us, as float32 121);
+  // with two as float32, since the same reads serve both (193 us, widened at each use 201).
+  typedef typename std::conditional<CH == 1, typename Two<TI>::raw, f2>::type bc2;
+  static constexpr int kPairBC = N * (int)sizeof(bc2);
+  static constexpr int kBC = (kOut ? 4 : 2) * (TT / 2) * kPairBC;
   static constexpr int kY = kOut ? 2 * TT * CT * 4 : 0;
   static constexpr int kSmem = kDx + kBC + kY;
 };
@@ -167,12 +176,11 @@ template <int L> struct LaneSums {
 
 // Part blockIdx.y of a sequence: kOut writes y (and, in the last part, hT);
 // else only the state that the part leaves.
-template <typename TI, int N, class X, bool kOut>
-__global__ void __launch_bounds__(ScanShape<N, X, kOut>::kThreads, 2)
+template <typename TI, int N, int CH, bool kOut>
+__global__ void __launch_bounds__(ScanShape<TI, N, CH, kOut>::kThreads, 2)
 selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
-  using S = ScanShape<N, X, kOut>;
+  using S = ScanShape<TI, N, CH, kOut>;
   constexpr int L = S::L, CT = S::CT, TT = S::TT;
-  constexpr int CH = X::CH, PER = X::PER, kRec = X::REC, kIo = X::IO;
   extern __shared__ __align__(16) char smem[];
   char *dx = smem;
   char *bc = dx + S::kDx;
@@ -196,53 +204,55 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 
   const int tid = threadIdx.x;
   if (tid < kRec) {
-    // ---- recurrence: L lanes of PER entries share CH channels
-    const int ch = tid / L * CH, lane = tid % L, n0 = lane * PER;
+    // ---- recurrence: L lanes of kPer entries share CH channels
+    const int ch = tid / L * CH, lane = tid % L, n0 = lane * kPer;
     const long long plane = (long long)a.B * a.D * N;
-    f2 A2[CH][PER];  // both halves A log2 e
-    float h[CH][PER];
+    f2 A2[CH][kPer];  // both halves A log2 e
+    float h[CH][kPer];
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       const bool live = ch + j < chans;
       const int c = c0 + (live ? ch + j : 0);
-#pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        const long long so = ((long long)b * a.D + c) * N + n0 + 4 * i;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), s = v;
-        if (live) v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + n0 + 4 * i);
-        v.x *= kLog2e, v.y *= kLog2e, v.z *= kLog2e, v.w *= kLog2e;
-        if (part == 0) {
-          // (a split sequence takes h0 from its copy: the last part may have written hT over it)
-          const float *from = kOut && p.split > 1 ? p.state : a.h0;
-          if (live && from) s = *reinterpret_cast<const float4 *>(from + so);
-          if (!kOut && live) *reinterpret_cast<float4 *>(p.state + so) = s;
-        } else if (kOut && live) {
-          // the state at the part's start, from what the parts before left
-          s = *reinterpret_cast<const float4 *>(p.state + plane + so);
-          for (int k = 1; k < part; ++k) {
-            const float sum = p.sum[((long long)k * a.B + b) * a.D + c];
-            const float4 e = *reinterpret_cast<const float4 *>(p.state + (k + 1) * plane + so);
-            s.x = fmaf(ex2(sum * v.x), s.x, e.x), s.y = fmaf(ex2(sum * v.y), s.y, e.y);
-            s.z = fmaf(ex2(sum * v.z), s.z, e.z), s.w = fmaf(ex2(sum * v.w), s.w, e.w);
-          }
+      const long long so = ((long long)b * a.D + c) * N + n0;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f), s = v;
+      if (live) v = *reinterpret_cast<const float4 *>(a.A + (long long)c * N + n0);
+      v.x *= kLog2e, v.y *= kLog2e, v.z *= kLog2e, v.w *= kLog2e;
+      if (part == 0) {
+        // (a split sequence takes h0 from its copy: the last part may have written hT over it)
+        const float *from = kOut && p.split > 1 ? p.state : a.h0;
+        if (live && from) s = *reinterpret_cast<const float4 *>(from + so);
+        if (!kOut && live) *reinterpret_cast<float4 *>(p.state + so) = s;
+      } else if (kOut && live) {
+        // the state at the part's start, from what the parts before left
+        s = *reinterpret_cast<const float4 *>(p.state + plane + so);
+        for (int k = 1; k < part; ++k) {
+          const float sum = p.sum[((long long)k * a.B + b) * a.D + c];
+          const float4 e = *reinterpret_cast<const float4 *>(p.state + (k + 1) * plane + so);
+          s.x = fmaf(ex2(sum * v.x), s.x, e.x), s.y = fmaf(ex2(sum * v.y), s.y, e.y);
+          s.z = fmaf(ex2(sum * v.z), s.z, e.z), s.w = fmaf(ex2(sum * v.w), s.w, e.w);
         }
-        A2[j][4 * i] = both(v.x), A2[j][4 * i + 1] = both(v.y);
-        A2[j][4 * i + 2] = both(v.z), A2[j][4 * i + 3] = both(v.w);
-        h[j][4 * i] = s.x, h[j][4 * i + 1] = s.y, h[j][4 * i + 2] = s.z, h[j][4 * i + 3] = s.w;
       }
+      A2[j][0] = both(v.x), A2[j][1] = both(v.y), A2[j][2] = both(v.z), A2[j][3] = both(v.w);
+      h[j][0] = s.x, h[j][1] = s.y, h[j][2] = s.z, h[j][3] = s.w;
     }
     // A block is two items of one channel and two tokens: two pairs of tokens (CH = 1) or two
     // channels (CH = 2).  It gives the four values (token i / CH, channel i % CH) that LaneSums
     // takes.  A pair's operands are fetched while the one before is in work.
+    typedef typename S::bc2 bc2;
     struct Pair {
-      ulonglong2 d[CH], B[PER / 2], C[PER / 2];
+      ulonglong2 d[CH];
+      bc2 B[kPer], C[kPer];
+    };
+    const auto wide = [](const bc2 &v) {
+      if constexpr (std::is_same<bc2, f2>::value) return v;
+      else return Two<TI>::widen(v);
     };
     constexpr int TB = 4 / CH;
     float sum[CH] = {};
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
       const char *q = dx + (k & 1) * (TT / 2) * S::kPairRow + ch % 4 * S::kPlane + ch / 4 * 16;
-      const char *Bk = bc + ((k & 1) * TT * N + 2 * n0) * 4;
+      const char *Bk = bc + (k & 1) * (TT / 2) * S::kPairBC + n0 * (int)sizeof(bc2);
       // a lane stores kOwn values of a block
       constexpr int kOwn = L >= 4 ? 1 : 4 / L;
       float *yk = ys + (k & 1) * TT * CT + ch + lane % 4 * kOwn / CH * CT + lane % 4 * kOwn % CH;
@@ -250,11 +260,14 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 #pragma unroll
         for (int j = 0; j < CH; ++j)
           x.d[j] = *reinterpret_cast<const ulonglong2 *>(q + t / 2 * S::kPairRow + j * S::kPlane);
+        constexpr int kPieces = kPer * (int)sizeof(bc2) / 16;
 #pragma unroll
-        for (int n = 0; n < PER / 2; ++n) {
-          x.B[n] = *reinterpret_cast<const ulonglong2 *>(Bk + t * N * 4 + n * 16);
+        for (int i = 0; i < kPieces; ++i) {
+          const char *at = Bk + t / 2 * S::kPairBC + i * 16;
+          reinterpret_cast<uint4 *>(x.B)[i] = *reinterpret_cast<const uint4 *>(at);
           if (kOut)
-            x.C[n] = *reinterpret_cast<const ulonglong2 *>(Bk + (2 * TT + t) * N * 4 + n * 16);
+            reinterpret_cast<uint4 *>(x.C)[i] =
+                *reinterpret_cast<const uint4 *>(at + 2 * (TT / 2) * S::kPairBC);
         }
       };
       float tile_sum[CH] = {};
@@ -270,15 +283,14 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       const auto item = [&](const Pair &x, int j, int which) {
         f2 s = 0;
 #pragma unroll
-        for (int n = 0; n < PER; ++n) {
-          if (kOut && n % (PER / 2) == 0) sums.step(2 * which + n / (PER / 2), lane);
-          const ulonglong2 Bn = x.B[n / 2], Cn = x.C[n / 2];
+        for (int n = 0; n < kPer; ++n) {
+          if (kOut && n % (kPer / 2) == 0) sums.step(2 * which + n / (kPer / 2), lane);
           const float2 e = unpack(mul2(A2[j][n], x.d[j].x));
-          const float2 xb = unpack(mul2(x.d[j].y, n % 2 ? Bn.y : Bn.x));
+          const float2 xb = unpack(mul2(x.d[j].y, wide(x.B[n])));
           const float h0 = fmaf(ex2(e.x), h[j][n], xb.x);
           h[j][n] = fmaf(ex2(e.y), h0, xb.y);
           if (kOut) {
-            const f2 hh = pack(h0, h[j][n]), c = n % 2 ? Cn.y : Cn.x;
+            const f2 hh = pack(h0, h[j][n]), c = wide(x.C[n]);
             s = n ? fma2(hh, c, s) : mul2(hh, c);
           }
         }
@@ -324,12 +336,8 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       const int c = c0 + ch + j;
       const long long so = ((long long)b * a.D + c) * N + n0;
       float *to = kOut ? (last ? a.hT : nullptr) : p.state + (part + 1) * plane;
-#pragma unroll
-      for (int i = 0; i < PER / 4; ++i) {
-        if (to)
-          *reinterpret_cast<float4 *>(to + so + 4 * i) =
-              make_float4(h[j][4 * i], h[j][4 * i + 1], h[j][4 * i + 2], h[j][4 * i + 3]);
-      }
+      if (to)
+        *reinterpret_cast<float4 *>(to + so) = make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
       if (!kOut && n0 == 0) p.sum[((long long)part * a.B + b) * a.D + c] = sum[j];
     }
     return;
@@ -344,9 +352,9 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     return q ? pack(four > i ? q[c0 + ch + i] : 0.f, four > i + 1 ? q[c0 + ch + i + 1] : 0.f) : 0;
   };
   // The four channels of the thread's tokens, `rows` tokens before the end.
-  const auto rows_of = [&](Four<TI> (&v)[2], const TI *q, long long st, int rows, bool wide) {
-    v[0].load(q, 2 * pr < rows ? four : 0, wide);
-    v[1].load(q + st, 2 * pr + 1 < rows ? four : 0, wide);
+  const auto rows_of = [&](Four<TI> (&v)[2], const TI *q, long long st, int rows, int at_once) {
+    v[0].load(q, 2 * pr < rows ? four : 0, at_once);
+    v[1].load(q + st, 2 * pr + 1 < rows ? four : 0, at_once);
   };
   const auto place = [&](const Rows &x) {
     return static_cast<const TI *>(x.p) + b * x.sb + c0 + ch + (t0 + 2 * pr) * x.st;
@@ -358,34 +366,38 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     // ---- step sizes, B and C of the next tile, read one tile further ahead
     const TI *de = place(a.delta);
     Four<TI> rd[2];
-    // two values of B and C of two tokens: pair io / (N / 2) of a tile, kIo / (N / 2) pairs on
-    constexpr int kItems = TT / 2 * (N / 2), kQ = kItems > kIo ? kItems / kIo : 1;
+    // kWide values of B and C of two tokens: pair io / (N / kWide) of a tile, and kOn pairs on
+    constexpr int kWide = TT / 2 * (N / 2) > kIo ? 4 : 2, kOn = kIo / (N / kWide);
+    constexpr int kItems = TT / 2 * (N / kWide), kQ = kItems > kIo ? kItems / kIo : 1;
     static_assert(kItems <= kIo || kItems % kIo == 0, "whole rounds");
-    const int qp = io / (N / 2), qn = io % (N / 2) * 2;
+    const int qp = io / (N / kWide), qn = io % (N / kWide) * kWide;
     const bool has_item = qp < TT / 2;
     const auto group = [&](const Rows &x) {
       return static_cast<const TI *>(x.p) + b * x.sb + (long long)g * N + qn +
              (t0 + 2 * qp) * x.st;
     };
     const TI *Bm = group(a.Bm), *Cm = group(a.Cm);
-    typename Two<TI>::raw rB[kQ][2], rC[kQ][2];
+    Four<TI> rB[kQ][2], rC[kQ][2];  // of two tokens
     const f2 bias[2] = {per_channel(a.bias, 0), per_channel(a.bias, 2)};
-    const auto item = [&](typename Two<TI>::raw (&v)[2], const TI *q, long long st, int t, int rows,
-                          bool wide) {
-      v[0] = load_two<TI>(q, t < rows ? 2 : 0, wide);
-      v[1] = load_two<TI>(q + st, t + 1 < rows ? 2 : 0, wide);
-    };
     int ahead = t1 - t0;  // tokens from the tile that is read next to the end
+    const auto item = [&](Four<TI> (&v)[2], const TI *q, long long st, int t, int at_once) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (kWide == 4)
+          v[e].load(q + e * st, t + e < ahead ? 4 : 0, at_once);
+        else
+          v[e].v[0] = load_two<TI>(q + e * st, t + e < ahead ? 2 : 0, at_once >= 2);
+      }
+    };
     const auto load = [&]() {
-      rows_of(ru, u, a.u.st, ahead, p.vec & kVecU);
-      rows_of(rd, de, a.delta.st, ahead, p.vec & kVecDelta);
+      rows_of(ru, u, a.u.st, ahead, p.u_at_once);
+      rows_of(rd, de, a.delta.st, ahead, p.delta_at_once);
       if (has_item) {
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
-          const int t = 2 * (qp + i * (kIo / (N / 2)));
-          const long long on = 2 * i * (kIo / (N / 2));
-          item(rB[i], Bm + on * a.Bm.st, a.Bm.st, t, ahead, p.vec & kVecB);
-          if (kOut) item(rC[i], Cm + on * a.Cm.st, a.Cm.st, t, ahead, p.vec & kVecC);
+          const int t = 2 * (qp + i * kOn);
+          item(rB[i], Bm + 2 * i * kOn * a.Bm.st, a.Bm.st, t, p.B_at_once);
+          if (kOut) item(rC[i], Cm + 2 * i * kOn * a.Cm.st, a.Cm.st, t, p.C_at_once);
         }
       }
       u += TT * a.u.st, de += TT * a.delta.st, Bm += TT * a.Bm.st, Cm += TT * a.Cm.st, ahead -= TT;
@@ -416,15 +428,22 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
         }
       }
       if (has_item) {
-        float *fb = reinterpret_cast<float *>(bc) + (k & 1) * TT * N + qp * 2 * N + 2 * qn;
-        const auto put = [&](float *to, const typename Two<TI>::raw (&v)[2]) {
-          const float2 lo = unpack(Two<TI>::widen(v[0])), hi = unpack(Two<TI>::widen(v[1]));
-          *reinterpret_cast<float4 *>(to) = make_float4(lo.x, hi.x, lo.y, hi.y);
+        typedef typename S::bc2 bc2;
+        char *to = bc + ((k & 1) * (TT / 2) + qp) * S::kPairBC + qn * (int)sizeof(bc2);
+        const auto put = [&](char *at, const Four<TI> (&v)[2]) {
+          bc2 *o = reinterpret_cast<bc2 *>(at);
+#pragma unroll
+          for (int j = 0; j < kWide / 2; ++j) {
+            if constexpr (std::is_same<bc2, f2>::value)
+              Two<float>::trade(v[0].pair(j), v[1].pair(j), o[2 * j], o[2 * j + 1]);
+            else
+              Two<TI>::trade(v[0].v[j], v[1].v[j], o[2 * j], o[2 * j + 1]);
+          }
         };
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
-          put(fb + i * (kIo / (N / 2)) * 2 * N, rB[i]);
-          if (kOut) put(fb + 2 * TT * N + i * (kIo / (N / 2)) * 2 * N, rC[i]);
+          put(to + i * kOn * S::kPairBC, rB[i]);
+          if (kOut) put(to + (2 * (TT / 2) + i * kOn) * S::kPairBC, rC[i]);
         }
       }
     };
@@ -453,8 +472,8 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
   TI *y = static_cast<TI *>(a.y) + ((long long)b * a.T + t0 + 2 * pr) * a.D + c0 + ch;
   int rows = t1 - t0;  // tokens from the tile in work to the end
   const auto load = [&]() {
-    rows_of(ru, u, a.u.st, rows, p.vec & kVecU);
-    if (gated) rows_of(rz, z, a.z.st, rows, p.vec & kVecZ);
+    rows_of(ru, u, a.u.st, rows, p.u_at_once);
+    if (gated) rows_of(rz, z, a.z.st, rows, p.z_at_once);
     u += TT * a.u.st, z += TT * a.z.st;
   };
   const auto write = [&](int k) {
@@ -470,7 +489,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
           if (gated) v = mul2(v, silu2(rz[e].pair(i)));
           o.narrow(i, v);
         }
-        if (2 * pr + e < rows) o.store(y + (long long)e * a.D, four, p.vec & kVecY);
+        if (2 * pr + e < rows) o.store(y + (long long)e * a.D, four, p.y_at_once);
       }
     }
     y += (long long)TT * a.D, rows -= TT;
@@ -496,7 +515,7 @@ struct StepArgs {
   int n_slots;
   void *y;
   int R, D, G, softplus;
-  unsigned vec;  // whether B and C can be read four values at a time
+  int B_at_once, C_at_once;  // values read at once: 4, 2 or 1
   unsigned cblocks;
 };
 
@@ -533,8 +552,8 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
   const float z = gated ? Io<TI>::ld(static_cast<const TI *>(a.z.p) + r * a.z.sb + c) : 0.f;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    B[q].load(pB + q * (N / 2), 4, a.vec & kVecB);
-    C[q].load(pC + q * (N / 2), 4, a.vec & kVecC);
+    B[q].load(pB + q * (N / 2), 4, a.B_at_once);
+    C[q].load(pC + q * (N / 2), 4, a.C_at_once);
     A[q] = *reinterpret_cast<const float4 *>(a.A + e + q * (N / 2));
   }
   const float skip = a.Dskip ? a.Dskip[c] : 0.f;
@@ -565,7 +584,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
 }
 
 struct ScanChoice {
-  int cut, split;  // which Cut, parts of a sequence
+  int CH, split;  // channels per lane group, parts of a sequence
 };
 // Two channels per lane group halve the reads of B and C per entry, and the warps: worth it
 // once there are warps for two CTAs on every SM all the same (16384 channels of 16 entries,
@@ -577,7 +596,7 @@ struct ScanChoice {
 ScanChoice scan_choice(int B, int T, int D, int N) {
   const long long warps = ((long long)B * D * N + 127) / 128;  // with four entries per thread
   ScanChoice c;
-  c.cut = warps > kTargetWarps ? 2 : 1;
+  c.CH = warps > kTargetWarps ? 2 : 1;
   long long s = warps > 0 ? kTargetWarps / warps : 1;
   if (s > T / 64) s = T / 64;
   if (s > kMaxSplit) s = kMaxSplit;
@@ -591,28 +610,30 @@ template <class K> bool allow_smem(K *kernel, int bytes) {  // 48 KiB need no le
              cudaSuccess;
 }
 
-template <typename TI, int N, class X>
-kda_status launch_scan_cut(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
-  using So = ScanShape<N, X, true>;
-  using Ss = ScanShape<N, X, false>;
+template <typename TI, int N, int CH>
+kda_status launch_scan_ch(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
+  using So = ScanShape<TI, N, CH, true>;
   p.tiles_g = (a.D / a.G + So::CT - 1) / So::CT;
   const long long blocks = (long long)a.B * a.G * p.tiles_g;
   if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  if (!allow_smem(selective_scan_kernel<TI, N, X, true>, So::kSmem)) return KDA_ERR_CUDA;
-  if (p.split > 1) {
-    if (!allow_smem(selective_scan_kernel<TI, N, X, false>, Ss::kSmem)) return KDA_ERR_CUDA;
-    selective_scan_kernel<TI, N, X, false>
-        <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
+  if (!allow_smem(selective_scan_kernel<TI, N, CH, true>, So::kSmem)) return KDA_ERR_CUDA;
+  if constexpr (CH == 1) {  // what scan_choice splits has one channel per lane group
+    using Ss = ScanShape<TI, N, CH, false>;
+    if (p.split > 1) {
+      if (!allow_smem(selective_scan_kernel<TI, N, CH, false>, Ss::kSmem)) return KDA_ERR_CUDA;
+      selective_scan_kernel<TI, N, CH, false>
+          <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
+    }
   }
-  selective_scan_kernel<TI, N, X, true>
+  selective_scan_kernel<TI, N, CH, true>
       <<<dim3((unsigned)blocks, p.split), So::kThreads, So::kSmem, st>>>(a, p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 template <typename TI, int N>
-kda_status launch_scan(const ScanArgs &a, const ScanPlan &p, int cut, cudaStream_t st) {
-  if (cut == 2) return launch_scan_cut<TI, N, Cut<2, 4, 128, 128>>(a, p, st);
-  return launch_scan_cut<TI, N, Cut<1, 4, 128, 128>>(a, p, st);
+kda_status launch_scan(const ScanArgs &a, const ScanPlan &p, int CH, cudaStream_t st) {
+  return CH == 2 ? launch_scan_ch<TI, N, 2>(a, p, st) : launch_scan_ch<TI, N, 1>(a, p, st);
 }
+
 template <typename TI, int N>
 kda_status launch_step(StepArgs a, cudaStream_t st) {
   constexpr int kChans = kStepThreads / (N / 8);
@@ -624,12 +645,12 @@ kda_status launch_step(StepArgs a, cudaStream_t st) {
 }
 
 template <typename TI>
-kda_status launch_scan_n(const ScanArgs &a, const ScanPlan &p, int cut, int N, cudaStream_t st) {
+kda_status launch_scan_n(const ScanArgs &a, const ScanPlan &p, int CH, int N, cudaStream_t st) {
   switch (N) {
-    case 8: return launch_scan<TI, 8>(a, p, cut, st);
-    case 16: return launch_scan<TI, 16>(a, p, cut, st);
-    case 32: return launch_scan<TI, 32>(a, p, cut, st);
-    default: return launch_scan<TI, 64>(a, p, cut, st);
+    case 8: return launch_scan<TI, 8>(a, p, CH, st);
+    case 16: return launch_scan<TI, 16>(a, p, CH, st);
+    case 32: return launch_scan<TI, 32>(a, p, CH, st);
+    default: return launch_scan<TI, 64>(a, p, CH, st);
   }
 }
 template <typename TI>
@@ -644,6 +665,14 @@ kda_status launch_step_n(const StepArgs &a, int N, cudaStream_t st) {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 uintptr_t size_of(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
+
+// The most values, up to `most`, that the address and its strides are multiples of.
+int at_once(const void *p, const long long *strides, int n, int most, kda_dtype dt) {
+  uintptr_t all = reinterpret_cast<uintptr_t>(p);
+  for (int i = 0; i < n; ++i) all |= (uintptr_t)strides[i] * size_of(dt);
+  while (all % (most * size_of(dt)) != 0) most /= 2;
+  return most;
+}
 
 // Checks shared by the scan and the step: enums, flags, sizes.
 kda_status check_sizes(int B, int T, int D, int G, int N, kda_dtype dt, unsigned flags) {
@@ -704,19 +733,17 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
   p.tiles_g = 0;  // by the kernel's shape
   p.state = static_cast<float *>(workspace);
   p.sum = p.state + (size_t)p.split * B * D * N;
-  // wide accesses: the address and both strides are multiples of n values, and no row of a
-  // group ends inside four channels
-  const auto wide = [&](const void *q, int i, int n) {
-    return (reinterpret_cast<uintptr_t>(q) | (uintptr_t)(strides[i] * e) |
-            (uintptr_t)(strides[i + 1] * e)) % (n * e) == 0;
-  };
-  p.vec = (wide(Bm, 4, 2) ? kVecB : 0) | (wide(Cm, 6, 2) ? kVecC : 0);
-  if (D / G % 4 == 0)
-    p.vec |= (wide(u, 0, 4) ? kVecU : 0) | (wide(delta, 2, 4) ? kVecDelta : 0) |
-             (z && wide(z, 8, 4) ? kVecZ : 0) | kVecY;
+  // A thread's four channels end with their group, so what is read at once divides a group.
+  const int of_group = D / G % 4 == 0 ? 4 : D / G % 2 == 0 ? 2 : 1;
+  p.u_at_once = at_once(u, strides, 2, of_group, dt);
+  p.delta_at_once = at_once(delta, strides + 2, 2, of_group, dt);
+  p.B_at_once = at_once(Bm, strides + 4, 2, 4, dt);
+  p.C_at_once = at_once(Cm, strides + 6, 2, 4, dt);
+  p.z_at_once = z ? at_once(z, strides + 8, 2, of_group, dt) : 1;
+  p.y_at_once = of_group;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.cut, N, st)
-                        : launch_scan_n<float>(a, p, choice.cut, N, st);
+  return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.CH, N, st)
+                        : launch_scan_n<float>(a, p, choice.CH, N, st);
 }
 
 extern "C" kda_status kda_selective_step(const void *u, const void *delta, const float *A,
@@ -742,11 +769,7 @@ extern "C" kda_status kda_selective_step(const void *u, const void *delta, const
                    {Cm, strides[3], 0}, {z, z ? strides[4] : 0, 0},
                    A, Dskip, delta_bias, S, slots, n_slots, y, R, D, G,
                    (flags & KDA_SCAN_SOFTPLUS) != 0u,
-                   ((reinterpret_cast<uintptr_t>(Bm) | (uintptr_t)(strides[2] * e)) % (4 * e) == 0
-                        ? kVecB : 0) |
-                       ((reinterpret_cast<uintptr_t>(Cm) | (uintptr_t)(strides[3] * e)) % (4 * e) == 0
-                            ? kVecC : 0),
-                   0};
+                   at_once(Bm, strides + 2, 1, 4, dt), at_once(Cm, strides + 3, 1, 4, dt), 0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_step_n<__nv_bfloat16>(a, N, st) : launch_step_n<float>(a, N, st);
 }

@@ -214,6 +214,14 @@ def test_scan_long(B, T, D, G, N, dtype):
     _check_scan(scan_case(T, B, T, D, G, N, dtype, state=True), dtype)
 
 
+@pytest.mark.parametrize("B,T,D,G,N,dtype", [(40, 37, 1030, 2, 16, "bf16"), (80, 21, 640, 4, 8, "f32"),
+                                             (24, 40, 516, 3, 32, "f32"), (5, 33, 1000, 1, 64, "bf16")])
+def test_scan_many_channels(B, T, D, G, N, dtype):
+    """Enough channels that lane groups take two each; groups that end inside a CTA's channels."""
+    lens = [T] + [(7 * i) % (T + 1) for i in range(1, B)]
+    _check_scan(scan_case(B, B, T, D, G, N, dtype, state=True, lens=lens), dtype)
+
+
 def test_scan_long_padded():
     T = 3000
     _check_scan(scan_case(3, 3, T, 16, 1, 16, "bf16", state=True, lens=[5, 1777, T]), "bf16")
@@ -225,6 +233,35 @@ def test_scan_strong_decay_and_large_steps():
     c = scan_case(6, 1, 60, 16, 1, 16, "f32", bias=False)
     c["delta"] = np.random.default_rng(0).uniform(-30, 60, c["delta"].shape).astype(np.float32)
     _check_scan(c, "f32")
+
+
+@pytest.mark.parametrize("T", [70, 1300])
+def test_scan_infinite_steps_and_nan(T):
+    """delta = -inf gives softplus 0: the token neither decays nor adds, whatever
+    its finite u.  A NaN in one channel's u or delta reaches that channel, from
+    its token on, and no other; a NaN in z one output."""
+    c = scan_case(12, 2, T, 24, 1, 16, "f32", bias=False, state=True)
+    gone = np.arange(T) % 3 == 1
+    c["delta"][0, gone] = -np.inf
+    kept = {k: (v[:1, ~gone] if k in ("u", "delta", "Bm", "Cm", "z") else v) for k, v in c.items()}
+    kept["h0"] = c["h0"][:1]
+    c["u"][1, 20, 5] = np.nan
+    c["delta"][1, 40, 7] = np.nan
+    c["z"][1, 9, 2] = np.nan
+    t = _scan_tensors(c, "f32", False)
+    y, hT = kda.selective_scan(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"], t["z"],
+                               None, t["h0"])
+    torch.cuda.synchronize()
+    y, hT = host(y), host(hT)
+    yb, hb, ref, href = scan_bound(kept["u"], kept["delta"], c["A"], kept["Bm"], kept["Cm"], c["D"],
+                                   kept["z"], None, kept["h0"], None, True, "f32")
+    within(y[:1, ~gone], ref, yb, "y")
+    within(hT[:1], href, hb, "hT")
+    bad = np.zeros((T, 24), bool)
+    bad[20:, 5] = bad[40:, 7] = True
+    bad[9, 2] = True
+    assert np.array_equal(np.isnan(y[1]), bad) and np.isfinite(y[0]).all()
+    assert np.isnan(hT[1, [5, 7]]).all() and np.isnan(hT[1]).sum() == 2 * 16
 
 
 @pytest.mark.parametrize("N", [8, 16, 32, 64])
