@@ -39,7 +39,7 @@ constexpr int kRec = 128;          // recurrence threads of a CTA, kPer entries 
 constexpr int kIo = 128;           // threads that prepare operands, and as many that write y
 constexpr int kPer = 4;
 constexpr int kMaxSplit = 64;      // parts of a sequence
-constexpr int kTargetWarps = 1216; // 152 SMs x 4 schedulers x 2
+constexpr int kTargetWarps = 1216; // recurrence warps: 152 SMs x 4 schedulers x 2
 
 struct ScanPlan {
   float *state;  // [split][B][D][N]: 0: h0; j: what part j - 1 leaves (0 from h0, others from 0)
@@ -130,7 +130,8 @@ template <typename TI, int N, int CH, bool kOut> struct ScanShape {
   // write four channels as for the lanes that read neighbouring ones.
   static constexpr int kPlane = CT * 4 + 32, kPairRow = 4 * kPlane;
   static constexpr int kDx = 2 * (TT / 2) * kPairRow;
-  // B and C, [pair][n](token 0, token 1): with one channel per lane group as they are stored,
+  // B and C of a pair, (token 0, token 1) per n, a lane's four n in 16-byte pieces and the same
+  // piece of all lanes side by side: with one channel per lane group as they are stored,
   // since half the bytes leave shared memory then (8192 channels: 113 us, as float32 121);
   // with two as float32, since the same reads serve both (193 us, widened at each use 201).
   typedef typename std::conditional<CH == 1, typename Two<TI>::raw, f2>::type bc2;
@@ -252,7 +253,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     __syncthreads();
     for (int k = 0; k < tiles; ++k) {
       const char *q = dx + (k & 1) * (TT / 2) * S::kPairRow + ch % 4 * S::kPlane + ch / 4 * 16;
-      const char *Bk = bc + (k & 1) * (TT / 2) * S::kPairBC + n0 * (int)sizeof(bc2);
+      const char *Bk = bc + (k & 1) * (TT / 2) * S::kPairBC + lane * 16;
       // a lane stores kOwn values of a block
       constexpr int kOwn = L >= 4 ? 1 : 4 / L;
       float *yk = ys + (k & 1) * TT * CT + ch + lane % 4 * kOwn / CH * CT + lane % 4 * kOwn % CH;
@@ -263,7 +264,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
         constexpr int kPieces = kPer * (int)sizeof(bc2) / 16;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          const char *at = Bk + t / 2 * S::kPairBC + i * 16;
+          const char *at = Bk + t / 2 * S::kPairBC + i * (L * 16);
           reinterpret_cast<uint4 *>(x.B)[i] = *reinterpret_cast<const uint4 *>(at);
           if (kOut)
             reinterpret_cast<uint4 *>(x.C)[i] =
@@ -429,15 +430,20 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       }
       if (has_item) {
         typedef typename S::bc2 bc2;
-        char *to = bc + ((k & 1) * (TT / 2) + qp) * S::kPairBC + qn * (int)sizeof(bc2);
+        char *to = bc + ((k & 1) * (TT / 2) + qp) * S::kPairBC;
         const auto put = [&](char *at, const Four<TI> (&v)[2]) {
-          bc2 *o = reinterpret_cast<bc2 *>(at);
 #pragma unroll
           for (int j = 0; j < kWide / 2; ++j) {
-            if constexpr (std::is_same<bc2, f2>::value)
-              Two<float>::trade(v[0].pair(j), v[1].pair(j), o[2 * j], o[2 * j + 1]);
-            else
-              Two<TI>::trade(v[0].v[j], v[1].v[j], o[2 * j], o[2 * j + 1]);
+            const int n = qn + 2 * j;
+            alignas(16) bc2 o[2];
+            if constexpr (std::is_same<bc2, f2>::value) {
+              Two<float>::trade(v[0].pair(j), v[1].pair(j), o[0], o[1]);
+              *reinterpret_cast<uint4 *>(at + (n % 4 / 2 * L + n / 4) * 16) =
+                  *reinterpret_cast<const uint4 *>(o);
+            } else {
+              Two<TI>::trade(v[0].v[j], v[1].v[j], o[0], o[1]);
+              *reinterpret_cast<uint2 *>(at + n * 4) = *reinterpret_cast<const uint2 *>(o);
+            }
           }
         };
 #pragma unroll
@@ -586,21 +592,33 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
 struct ScanChoice {
   int CH, split;  // channels per lane group, parts of a sequence
 };
-// Two channels per lane group halve the reads of B and C per entry, and the warps: worth it
-// once there are warps for two CTAs on every SM all the same (16384 channels of 16 entries,
-// 2048 tokens: 193 against 236 us; 8192 channels: 131 against 121; 4096 channels, 16384
-// tokens: 988 against 524).  Where one channel per group leaves most schedulers empty, the
-// tokens are split as well, at the price of the exponentials of a second pass: 1536 channels,
-// 8192 tokens: 6 parts 130 us, one 271 us; 4096 channels, 16384 tokens: 4 parts 703 us, one
-// 524 us, so two parts never pay.
-ScanChoice scan_choice(int B, int T, int D, int N) {
-  const long long warps = ((long long)B * D * N + 127) / 128;  // with four entries per thread
-  ScanChoice c;
-  c.CH = warps > kTargetWarps ? 2 : 1;
-  long long s = warps > 0 ? kTargetWarps / warps : 1;
+// One channel per lane group, or two (half the CTAs, and half the reads of B and C per entry)?
+// An SM holds two CTAs, so a launch runs in rounds of 304 whose last is shorter where it leaves
+// one CTA to an SM.  Nanoseconds per token of a full and of such a round, measured at 8 to 64
+// states (bf16, one channel: 54 to 60 and 31; two: 88 to 110 and 60 to 70).  What it decides,
+// bf16, 16 states, 1024 tokens, one against two channels: 8192 channels 57 against 65 us,
+// 12288: 93 / 105, 16384: 118 / 105, 20480: 146 / 159.
+//
+// Where one channel per group leaves most schedulers empty, the tokens are split as well, at the
+// price of the exponentials of a second pass: 1536 channels, 8192 tokens: 6 parts 127 us, one
+// 258 us; 4096 channels, 16384 tokens: 4 parts 675 us, one 513 us, so two parts never pay.
+ScanChoice scan_choice(int B, int T, int D, int G, int N, kda_dtype dt) {
+  const auto rounds = [&](int CH, int full, int last) {
+    const int CT = kRec / (N / kPer) * CH;
+    const long long ctas = (long long)B * G * ((D / G + CT - 1) / CT), rest = ctas % 304;
+    return ctas / 304 * full + (rest > 152 ? full : rest > 0 ? last : 0);
+  };
+  ScanChoice c{1, 1};
+  const long long warps = ((long long)B * D * N + 127) / 128;
+  long long s = kTargetWarps / (warps > 0 ? warps : 1);
   if (s > T / 64) s = T / 64;
   if (s > kMaxSplit) s = kMaxSplit;
-  c.split = s < 3 ? 1 : (int)s;
+  if (s >= 3)
+    c.split = (int)s;
+  else if (dt == KDA_BF16)
+    c.CH = rounds(2, 100, 65) < rounds(1, 57, 31) ? 2 : 1;
+  else
+    c.CH = rounds(2, 101, 66) < rounds(1, 66, 40) ? 2 : 1;
   return c;
 }
 
@@ -692,7 +710,7 @@ extern "C" size_t kda_selective_scan_workspace_size(int B, int T, int D, int G, 
   using namespace kda;
   if (check_sizes(B, T, D, G, N, dt, 0u) != KDA_OK) return 0;
   if (B == 0) return 256;
-  const size_t split = (size_t)scan_choice(B, T, D, N).split;
+  const size_t split = (size_t)scan_choice(B, T, D, G, N, dt).split;
   return 256 + (split > 1 ? split * B * D * (N + 1) * sizeof(float) : 0);
 }
 
@@ -726,7 +744,7 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
                    A, Dskip, delta_bias, h0, lens, y, hT, B, T, D, G,
                    (flags & KDA_SCAN_SOFTPLUS) != 0u};
   ScanPlan p;
-  const ScanChoice choice = scan_choice(B, T, D, N);
+  const ScanChoice choice = scan_choice(B, T, D, G, N, dt);
   p.split = choice.split;
   // a part is whole tiles, so its tokens need no masks but at the sequence's end
   p.part = (T + p.split * 32 - 1) / (p.split * 32) * 32;
