@@ -313,6 +313,12 @@ KERNEL_SOURCES = {
     "kda_scan_kernel": ["kda_chunk_tc.cu"] + _TC_HEADERS,
     "kda_scan_wide_kernel": ["kda_chunk_tc.cu"] + _TC_HEADERS,
     "attn_res_kernel": ["kda_attnres.cu", "kda_internal.cuh"],
+    "short_conv_kernel": ["kda_short_conv.cu", "kda_internal.cuh", "kda_pack.cuh"],
+    "short_conv_step_kernel": ["kda_short_conv.cu", "kda_internal.cuh", "kda_pack.cuh"],
+    "selective_scan_kernel": ["kda_selective.cu", "kda_internal.cuh", "kda_pack.cuh"],
+    "selective_step_kernel": ["kda_selective.cu", "kda_internal.cuh", "kda_pack.cuh"],
+    "state_copy_kernel": ["kda_state.cu"],
+    "state_clear_kernel": ["kda_state.cu"],
 }
 
 
@@ -506,12 +512,11 @@ def kda_selective_scan_workspace_size(B, T, D, G, N, dtype) -> int:
 
 
 def selective_scan_workspace_for(u, A, B):
-    """Workspace for ``kda_selective_scan`` on u [B,T,D], A [D,N], B [B,T,G,N]."""
+    """Workspace for ``kda_selective_scan`` on u [B,T,D], A [D,N], B [B,T,G,N],
+    or None where the call needs none."""
     n = kda_selective_scan_workspace_size(u.shape[0], u.shape[1], u.shape[2], B.shape[2],
                                           A.shape[1], _dtype_code(u))
-    if n == 0:
-        raise KdaError(KDA_ERR_UNSUPPORTED, "kda_selective_scan_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=u.device)
+    return torch.empty(n, dtype=torch.uint8, device=u.device) if n else None
 
 
 def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, workspace,
@@ -536,7 +541,7 @@ def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, wor
           _dense(h0, "h0", (nB, nD, N), f32, dev), _dense(lens, "lens", (nB,), torch.int32, dev),
           _dense(y, "y", rows, dt, dev), _dense(hT, "hT", (nB, nD, N), f32, dev), st, nB, T, nD,
           G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+          0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
 def selective_scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, h0=None, lens=None,

@@ -684,10 +684,12 @@ kda_status launch_step_n(const StepArgs &a, int N, cudaStream_t st) {
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 uintptr_t size_of(kda_dtype dt) { return dt == KDA_BF16 ? 2 : 4; }
 
-// The most values, up to `most`, that the address and its strides are multiples of.
-int at_once(const void *p, const long long *strides, int n, int most, kda_dtype dt) {
+// The most values, up to `most`, that an address and the strides in use are multiples of.
+int at_once(const void *p, int rows, long long sb, int tokens, long long st, int most,
+            kda_dtype dt) {
   uintptr_t all = reinterpret_cast<uintptr_t>(p);
-  for (int i = 0; i < n; ++i) all |= (uintptr_t)strides[i] * size_of(dt);
+  if (rows > 1) all |= (uintptr_t)sb * size_of(dt);
+  if (tokens > 1) all |= (uintptr_t)st * size_of(dt);
   while (all % (most * size_of(dt)) != 0) most /= 2;
   return most;
 }
@@ -708,10 +710,9 @@ kda_status check_sizes(int B, int T, int D, int G, int N, kda_dtype dt, unsigned
 extern "C" size_t kda_selective_scan_workspace_size(int B, int T, int D, int G, int N,
                                                     kda_dtype dt) {
   using namespace kda;
-  if (check_sizes(B, T, D, G, N, dt, 0u) != KDA_OK) return 0;
-  if (B == 0) return 256;
+  if (check_sizes(B, T, D, G, N, dt, 0u) != KDA_OK || B == 0) return 0;
   const size_t split = (size_t)scan_choice(B, T, D, G, N, dt).split;
-  return 256 + (split > 1 ? split * B * D * (N + 1) * sizeof(float) : 0);
+  return split > 1 ? split * B * D * (N + 1) * sizeof(float) : 0;
 }
 
 extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const float *A,
@@ -733,8 +734,8 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
       !aligned(z, e) || !aligned(A, 16) || !aligned(Dskip, 16) || !aligned(delta_bias, 16) ||
       !aligned(h0, 16) || !aligned(lens, 4) || !aligned(y, 16) || !aligned(hT, 16))
     return KDA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < kda_selective_scan_workspace_size(B, T, D, G, N, dt))
+  const size_t need = kda_selective_scan_workspace_size(B, T, D, G, N, dt);
+  if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < need))
     return KDA_ERR_INVALID_ARG;
   const ScanArgs a{{u, strides[0], strides[1]},
                    {delta, strides[2], strides[3]},
@@ -753,11 +754,14 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
   p.sum = p.state + (size_t)p.split * B * D * N;
   // A thread's four channels end with their group, so what is read at once divides a group.
   const int of_group = D / G % 4 == 0 ? 4 : D / G % 2 == 0 ? 2 : 1;
-  p.u_at_once = at_once(u, strides, 2, of_group, dt);
-  p.delta_at_once = at_once(delta, strides + 2, 2, of_group, dt);
-  p.B_at_once = at_once(Bm, strides + 4, 2, 4, dt);
-  p.C_at_once = at_once(Cm, strides + 6, 2, 4, dt);
-  p.z_at_once = z ? at_once(z, strides + 8, 2, of_group, dt) : 1;
+  const auto of = [&](const void *q, int i, int most) {
+    return at_once(q, B, strides[i], T, strides[i + 1], most, dt);
+  };
+  p.u_at_once = of(u, 0, of_group);
+  p.delta_at_once = of(delta, 2, of_group);
+  p.B_at_once = of(Bm, 4, 4);
+  p.C_at_once = of(Cm, 6, 4);
+  p.z_at_once = z ? of(z, 8, of_group) : 1;
   p.y_at_once = of_group;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.CH, N, st)
@@ -787,7 +791,8 @@ extern "C" kda_status kda_selective_step(const void *u, const void *delta, const
                    {Cm, strides[3], 0}, {z, z ? strides[4] : 0, 0},
                    A, Dskip, delta_bias, S, slots, n_slots, y, R, D, G,
                    (flags & KDA_SCAN_SOFTPLUS) != 0u,
-                   at_once(Bm, strides + 2, 1, 4, dt), at_once(Cm, strides + 3, 1, 4, dt), 0};
+                   at_once(Bm, R, strides[2], 1, 0, 4, dt),
+                   at_once(Cm, R, strides[3], 1, 0, 4, dt), 0};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_step_n<__nv_bfloat16>(a, N, st) : launch_step_n<float>(a, N, st);
 }

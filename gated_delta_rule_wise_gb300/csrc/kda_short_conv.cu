@@ -383,7 +383,10 @@ extern "C" kda_status kda_short_conv(const void *x, long long x_sb, long long x_
     return KDA_ERR_INVALID_ARG;
   if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
   if ((long long)B * H == 0 || (T == 0 && !sT)) return KDA_OK;
-  if (!w || (T > 0 && (!x || !y))) return KDA_ERR_INVALID_ARG;
+  if (!w || (T > 0 && (!x || !y || x == y))) return KDA_ERR_INVALID_ARG;
+  if (B == 1) x_sb = 0;  // strides that are not used do not count against wide reads
+  if (H == 1) x_sh = 0;
+  if (T <= 1) x_st = 0;
   if (!aligned(x, size_of(dt)) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(s0, 16) ||
       !aligned(lens, 4) || !aligned(y, 16) || !aligned(sT, 16))
     return KDA_ERR_INVALID_ARG;
@@ -413,6 +416,8 @@ extern "C" kda_status kda_short_conv_step(const void *x, long long x_sn, long lo
   if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED;
   if ((long long)N * H == 0 || n_slots == 0) return KDA_OK;
   if (!x || !w || !S || !y) return KDA_ERR_INVALID_ARG;
+  if (N == 1) x_sn = 0;
+  if (H == 1) x_sh = 0;
   if (!aligned(x, size_of(dt)) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(S, 16) ||
       !aligned(slots, 4) || !aligned(y, 16))
     return KDA_ERR_INVALID_ARG;

@@ -384,7 +384,8 @@ kda_status kda_decode_step(const void *q, const void *k, const void *v,
  *   lens  [B]             int32 (device), or NULL: row b has lens[b] tokens
  *                         (clamped to [0, T]); tokens behind them are not read
  *                         and their rows of y are left as they were
- *   y     [B, H, T, d]    dtype dt, contiguous (written; must not overlap x)
+ *   y     [B, H, T, d]    dtype dt, contiguous (written; must not overlap x,
+ *                         and y == x is refused: later tokens read x)
  *   sT    [B, H, W-1, d]  dtype dt, or NULL (written; may equal s0)
  *   W in {2, 3, 4}, else KDA_ERR_UNSUPPORTED; any d >= 1.  Sums in float32,
  *   rounded once.  x needs only its element's alignment; 16-byte aligned rows
@@ -440,7 +441,9 @@ kda_status kda_short_conv_step(const void *x, long long x_sn, long long x_sh, co
  *   divides D.
  *   workspace   >= kda_selective_scan_workspace_size(...) bytes of device
  *               memory, 256-byte aligned, not shared with a concurrent call;
- *               it needs no initialisation.
+ *               it needs no initialisation.  0 bytes (the tokens are not
+ *               split over CTAs, or the arguments are not supported): may be
+ *               NULL
  *
  * State and sums in float32; y rounded once.  The strided inputs need only
  * their element's alignment.
@@ -484,8 +487,9 @@ kda_status kda_selective_step(const void *u, const void *delta, const float *A, 
  * kda_state_copy: slot dst[i] receives slot src[i], for i = 0 .. n-1 with the
  * effect of that order: a pair may read what an earlier one wrote, and a slot
  * may occur any number of times on either side.  src[i] == dst[i] does
- * nothing.  Lists in which no pair touches what another writes (forks, moves
- * into free slots) run all at once.
+ * nothing.  Pairs none of which touches what another writes (forks, moves into
+ * free slots) run at once, 448 to a launch; a pair that does starts the next
+ * launch.
  * kda_state_clear: the listed slots are filled with zero bytes.
  * layers, n_slots, n >= 0; slot_bytes >= 0; layer_stride >= n_slots *
  * slot_bytes where layers > 1.  The pool needs no alignment beyond its element;

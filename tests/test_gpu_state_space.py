@@ -346,6 +346,33 @@ def test_state_clear(shape, dtype, layered):
     assert (v[:, ~keep.cuda()] == 0).all() and (v[:, keep.cuda()] == 1).all()
 
 
+def test_state_copy_of_an_unaligned_pool():
+    """A pool that starts one element into its storage moves in smaller pieces."""
+    base = torch.arange(1 + 6 * 40, device="cuda").to(torch.bfloat16)
+    pool = base[1:].view(6, 40)
+    want = pool.clone()
+    want[5], want[0] = pool[2], pool[3]
+    kda.state_copy(pool, [2, 3], [5, 0])
+    assert torch.equal(pool, want) and base[0] == 0
+
+
+def test_calls_on_given_streams():
+    """A torch stream, a raw handle and the legacy default stream (0)."""
+    x, w = torch.randn((1, 2, 50, 16), device="cuda"), torch.randn((2, 16, 4), device="cuda")
+    want, s_want = kda.short_conv(x, w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        y, sT = kda.short_conv(x, w, stream=stream)
+        pool = torch.zeros((3, 8), device="cuda")
+        torch.cuda.synchronize()
+        pool[1] = 5.0
+        torch.cuda.synchronize()
+        kda.state_copy(pool, [1], [2], stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(sT, s_want) and (pool[2] == 5).all()
+
+
 def test_state_copy_strided_layers():
     """Layers of a pool that lie further apart than their slots need."""
     wide = torch.arange(3 * 7 * 10, device="cuda", dtype=torch.float32).view(3, 7, 10)

@@ -82,7 +82,7 @@ def test_scan_definition_is_linear_attention_when_the_decay_is_shared():
 
 
 def _conv(lib, **kw):
-    a = dict(x=FAKE, sb=0, sh=0, st=0, w=FAKE, bias=None, s0=None, lens=None, y=FAKE, sT=FAKE, B=1,
+    a = dict(x=FAKE, sb=0, sh=0, st=0, w=FAKE, bias=None, s0=None, lens=None, y=FAKE + 512, sT=FAKE, B=1,
              H=1, T=4, d=8, W=4, dt=0, act=1, stream=None)
     a.update(kw)
     return lib.kda_short_conv(*a.values())
@@ -93,6 +93,7 @@ def test_conv_refuses_before_any_launch(lib):
     assert _conv(lib, B=-1) == INV and _conv(lib, d=0) == INV and _conv(lib, T=-1) == INV
     assert _conv(lib, st=-1) == INV and _conv(lib, sb=-8) == INV
     assert _conv(lib, W=5) == UNS and _conv(lib, W=1) == UNS
+    assert _conv(lib, y=FAKE + 256, x=FAKE + 256) == INV  # in place: later tokens read x
     assert _conv(lib, x=None) == INV and _conv(lib, w=None) == INV and _conv(lib, y=None) == INV
     assert _conv(lib, x=FAKE + 2) == INV               # not a float32 address
     assert _conv(lib, x=FAKE + 1, dt=1) == INV
@@ -129,7 +130,7 @@ def test_scan_refuses_before_any_launch(lib):
     assert call(dt=2) == INV and call(flags=2) == INV and call(B=-1) == INV and call(T=-1) == INV
     assert call(Dn=0) == INV and call(G=0) == INV and call(G=3) == INV
     assert call(N=12) == UNS and call(N=128) == UNS
-    for k in ("u", "delta", "A", "Bm", "Cm", "y", "st", "ws"):
+    for k in ("u", "delta", "A", "Bm", "Cm", "y", "st"):
         assert call(**{k: None}) == INV, k
     for k in ("A", "D", "db", "h0", "y", "hT"):
         assert call(**{k: FAKE + 4}) == INV, k
@@ -139,11 +140,16 @@ def test_scan_refuses_before_any_launch(lib):
         st = [0] * 10
         st[i] = -1
         assert call(st=st, z=FAKE) == INV, i
-    assert call(ws=FAKE + 16) == INV and call(wsb=16) == INV
     assert call(B=0) == OK and call(T=0, hT=None) == OK
     ws = lib.kda_selective_scan_workspace_size
-    assert ws(1, 4, 8, 2, 16, 0) >= 256 and ws(1, 4, 8, 3, 16, 0) == 0 and ws(1, 4, 8, 1, 4, 0) == 0
-    assert ws(1, 0, 8, 1, 16, 1) >= 256 and ws(0, 4, 8, 1, 16, 1) >= 256
+    # few channels and many tokens: the parts' states and step sums; else nothing
+    need = ws(1, 5000, 64, 2, 16, 0)
+    parts = need // (4 * 64 * 17)
+    assert need == parts * 4 * 64 * 17 and 3 <= parts <= 64
+    for bad in (dict(ws=None), dict(ws=FAKE + 16), dict(wsb=need - 1)):
+        assert call(T=5000, Dn=64, **bad) == INV, bad
+    assert ws(1, 4, 8, 2, 16, 0) == ws(8, 5000, 4096, 1, 16, 1) == ws(0, 5000, 64, 1, 16, 1) == 0
+    assert ws(1, 5000, 64, 3, 16, 0) == ws(1, 5000, 64, 1, 4, 0) == ws(1, 5000, 64, 1, 16, 7) == 0
 
 
 def test_step_refuses_before_any_launch(lib):
