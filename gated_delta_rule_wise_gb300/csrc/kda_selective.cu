@@ -19,6 +19,14 @@ namespace {
 
 constexpr int kStepThreads = 128;
 
+// ex2 is low by 0.09 to 0.48 of 2^-24 on average for exponents between -1e-4 and -1 (measured
+// over 2^21 arguments in each of eleven ranges), and a state of long memory adds that up over
+// its tokens.  Raised by 0.2 2^-24 / ln 2, at no cost inside the fma that forms the exponent,
+// the means lie between -0.26 and +0.11.  A step of 0 still gives 1: half a step of float32
+// above 1 is further away.
+constexpr float kRaise = 0.2f * 5.9604645e-08f * kLog2e;
+__device__ __forceinline__ f2 exponent2(f2 A2, f2 dt) { return fma2(A2, dt, both(kRaise)); }
+
 struct Rows {  // a strided input: batch and token stride in elements
   const void *p;
   long long sb, st;
@@ -286,7 +294,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 #pragma unroll
         for (int n = 0; n < kPer; ++n) {
           if (kOut && n % (kPer / 2) == 0) sums.step(2 * which + n / (kPer / 2), lane);
-          const float2 e = unpack(mul2(A2[j][n], x.d[j].x));
+          const float2 e = unpack(exponent2(A2[j][n], x.d[j].x));
           const float2 xb = unpack(mul2(x.d[j].y, wide(x.B[n])));
           const float h0 = fmaf(ex2(e.x), h[j][n], xb.x);
           h[j][n] = fmaf(ex2(e.y), h0, xb.y);
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const f2 A0 = mul2(pack(A[q].x, A[q].y), both(kLog2e)), A1 = mul2(pack(A[q].z, A[q].w), both(kLog2e));
-    const float2 e0 = unpack(mul2(A0, step)), e1 = unpack(mul2(A1, step));
+    const float2 e0 = unpack(exponent2(A0, step)), e1 = unpack(exponent2(A1, step));
     const f2 h0 = fma2(pack(ex2(e0.x), ex2(e0.y)), pack(s[q].x, s[q].y), mul2(xu, B[q].pair(0)));
     const f2 h1 = fma2(pack(ex2(e1.x), ex2(e1.y)), pack(s[q].z, s[q].w), mul2(xu, B[q].pair(1)));
     sum = q ? fma2(h0, C[q].pair(0), sum) : mul2(h0, C[q].pair(0));

@@ -235,6 +235,20 @@ def test_scan_strong_decay_and_large_steps():
     _check_scan(c, "f32")
 
 
+def test_scan_without_decay_keeps_its_state():
+    """A = 0, and steps of 0: the state keeps its bits however long the sequence."""
+    T, D = 5000, 32
+    c = scan_case(13, 1, T, D, 1, 16, "f32", bias=False, state=True, use_softplus=False)
+    t = _scan_tensors(c, "f32", False)
+    zero = torch.zeros_like
+    for delta, A, u in ((t["delta"], zero(t["A"]), zero(t["u"])), (zero(t["delta"]), t["A"], t["u"])):
+        _, hT = kda.selective_scan(u, delta, A, t["Bm"], t["Cm"], h0=t["h0"], softplus=False)
+        assert torch.equal(hT, t["h0"])
+        S = t["h0"].clone()
+        kda.selective_step(u[:, 0], delta[:, 0], A, t["Bm"][:, 0], t["Cm"][:, 0], S, softplus=False)
+        assert torch.equal(S, t["h0"])
+
+
 @pytest.mark.parametrize("T", [70, 1300])
 def test_scan_infinite_steps_and_nan(T):
     """delta = -inf gives softplus 0: the token neither decays nor adds, whatever
