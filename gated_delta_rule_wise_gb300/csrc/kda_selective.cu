@@ -185,6 +185,20 @@ template <int L> struct LaneSums {
 
 // Part blockIdx.y of a sequence: kOut writes y (and, in the last part, hT);
 // else only the state that the part leaves.
+//
+// Every (token, channel, n) costs an exponential and four float32 products or
+// sums, so the exponential unit (32 a clock and SM) and the float32 lanes (128)
+// bound the scan alike, at about 9.2e12 entries a second, before HBM does at 16
+// states: 117 us for 16384 tokens of 4096 channels, against 80 us for the bytes.
+// No matrix form: the decay between two tokens is another one for every
+// (channel, n).  One pass with the state in registers, cut so that both units are
+// fed by few warps: four recurrence warps hold the state, lanes of a channel
+// side by side; four warps turn the next tile of inputs into what the recurrence
+// reads (step sizes, dt u, B and C) in shared memory; four add D u, gate and store
+// the tile before.  A tile has one barrier.  Measured (bf16): 523 us for that
+// prompt (4096 channels are 3.4 recurrence warps per SM, so their latency shows:
+// issue 0.59 per cycle of a busy scheduler), 201 us for 4 x 2048 tokens of 4096
+// channels (issue 0.61, shared memory 56 %, the exponential unit 33 % of its rate).
 template <typename TI, int N, int CH, bool kOut>
 __global__ void __launch_bounds__(ScanShape<TI, N, CH, kOut>::kThreads, 2)
 selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
