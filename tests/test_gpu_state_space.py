@@ -528,6 +528,42 @@ def test_capture_and_replay_and_other_stream():
         assert torch.equal(a, b)
 
 
+def test_offsets_past_32_bits():
+    """Pools and outputs of more than 2^31 values: the highest slots and rows get
+    what the lowest get.  Inputs are one row read through a batch stride of 0."""
+    D, N, P = 4096, 16, 2 ** 31 // (4096 * 16) + 5
+    pool = torch.empty((P, D, N), device="cuda")
+    c = scan_case(41, 2, 1, D, 1, N, "bf16")
+    t = _scan_tensors({**c, "h0": None, "lens": None}, "bf16", False)
+    pool[[0, P - 1]] = 0.25
+    row = {k: t[k][:1, 0].expand((2,) + t[k].shape[2:]) for k in ("u", "delta", "Bm", "Cm", "z")}
+    y = kda.selective_step(row["u"], row["delta"], t["A"], row["Bm"], row["Cm"], pool, t["D"],
+                           row["z"], t["delta_bias"],
+                           torch.tensor([0, P - 1], dtype=torch.int32, device="cuda"))
+    kda.state_copy(pool, [P - 1], [P - 2])
+    assert torch.equal(y[0], y[1]) and torch.equal(pool[0], pool[P - 1])
+    assert torch.equal(pool[0], pool[P - 2]) and not torch.equal(pool[0], torch.full_like(pool[0], 0.25))
+    del pool
+
+    B, T = 3, 2 ** 31 // (2 * D) + 40
+    lens = torch.tensor([70, T, 70], dtype=torch.int32, device="cuda")
+    x = torch.randn((T, D), device="cuda", dtype=torch.bfloat16)
+    x[T - 70:] = x[:70]  # the last tokens as the first, after more zeros than there are taps
+    x[T - 80:T - 70] = 0
+    out = torch.empty((B, 1, T, D), dtype=torch.bfloat16, device="cuda")
+    kda.short_conv(x.expand(B, 1, T, D), torch.full((1, D, 4), 0.5, device="cuda"), None, None, lens,
+                   out=out)
+    assert torch.equal(out[0, 0, :70], out[1, 0, T - 70:]) and torch.equal(out[0, 0, :70], out[2, 0, :70])
+    out = out[:, 0]
+    steps = torch.ones((1, D), device="cuda", dtype=torch.bfloat16)  # a state lasts 40 tokens at most
+    BC = torch.ones((1, 1, N), device="cuda", dtype=torch.bfloat16)
+    _, hT = kda.selective_scan(x.expand(B, T, D), steps.expand(B, T, D), torch.full((D, N), -3.0, device="cuda"),
+                               BC.expand(B, T, 1, N), BC.expand(B, T, 1, N), lens=lens, softplus=False,
+                               out=out)
+    assert torch.equal(out[0, 40:70], out[2, 40:70]) and torch.equal(out[0, 40:70], out[1, T - 30:])
+    assert torch.equal(hT[0], hT[2]) and torch.equal(hT[0], hT[1])
+
+
 def test_scan_captured_and_replayed():
     c = scan_case(33, 2, 1500, 64, 1, 16, "bf16", state=True)
     t = _scan_tensors(c, "bf16", False)
