@@ -56,6 +56,7 @@ struct ScanPlan {
   int tiles_g;      // channel tiles of a group
   // how many values of a row can be read or written at once: 4, 2 or 1
   int u_at_once, delta_at_once, z_at_once, y_at_once, B_at_once, C_at_once;
+  bool wide;  // all of them 4: whole tiles then go without the questions
 };
 
 // n (0, 1, 2) values from p on; `wide`: both in one load.  What is missing is zero.
@@ -379,6 +380,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
     v[0].load(q, 2 * pr < rows ? four : 0, at_once);
     v[1].load(q + st, 2 * pr + 1 < rows ? four : 0, at_once);
   };
+  const bool wide = p.wide && four == 4;
   const auto place = [&](const Rows &x) {
     return static_cast<const TI *>(x.p) + b * x.sb + c0 + ch + (t0 + 2 * pr) * x.st;
   };
@@ -407,20 +409,31 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (kWide == 4)
-          v[e].load(q + e * st, t + e < ahead ? 4 : 0, at_once);
+          v[e].load(q + e * st, t < 0 || t + e < ahead ? 4 : 0, at_once);
         else
-          v[e].v[0] = load_two<TI>(q + e * st, t + e < ahead ? 2 : 0, at_once >= 2);
+          v[e].v[0] = load_two<TI>(q + e * st, t < 0 || t + e < ahead ? 2 : 0, at_once >= 2);
       }
     };
     const auto load = [&]() {
-      rows_of(ru, u, a.u.st, ahead, p.u_at_once);
-      rows_of(rd, de, a.delta.st, ahead, p.delta_at_once);
+      if (wide && ahead >= TT) {
+        ru[0].load(u, 4, 4), ru[1].load(u + a.u.st, 4, 4);
+        rd[0].load(de, 4, 4), rd[1].load(de + a.delta.st, 4, 4);
+      } else {
+        rows_of(ru, u, a.u.st, ahead, p.u_at_once);
+        rows_of(rd, de, a.delta.st, ahead, p.delta_at_once);
+      }
       if (has_item) {
 #pragma unroll
         for (int i = 0; i < kQ; ++i) {
           const int t = 2 * (qp + i * kOn);
-          item(rB[i], Bm + 2 * i * kOn * a.Bm.st, a.Bm.st, t, p.B_at_once);
-          if (kOut) item(rC[i], Cm + 2 * i * kOn * a.Cm.st, a.Cm.st, t, p.C_at_once);
+          const TI *B = Bm + 2 * i * kOn * a.Bm.st, *C = Cm + 2 * i * kOn * a.Cm.st;
+          if (p.wide && ahead >= TT) {
+            item(rB[i], B, a.Bm.st, -TT, 4);
+            if (kOut) item(rC[i], C, a.Cm.st, -TT, 4);
+          } else {
+            item(rB[i], B, a.Bm.st, t, p.B_at_once);
+            if (kOut) item(rC[i], C, a.Cm.st, t, p.C_at_once);
+          }
         }
       }
       u += TT * a.u.st, de += TT * a.delta.st, Bm += TT * a.Bm.st, Cm += TT * a.Cm.st, ahead -= TT;
@@ -500,8 +513,13 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
   TI *y = static_cast<TI *>(a.y) + ((long long)b * a.T + t0 + 2 * pr) * a.D + c0 + ch;
   int rows = t1 - t0;  // tokens from the tile in work to the end
   const auto load = [&]() {
-    rows_of(ru, u, a.u.st, rows, p.u_at_once);
-    if (gated) rows_of(rz, z, a.z.st, rows, p.z_at_once);
+    if (wide && rows >= TT) {
+      ru[0].load(u, 4, 4), ru[1].load(u + a.u.st, 4, 4);
+      if (gated) rz[0].load(z, 4, 4), rz[1].load(z + a.z.st, 4, 4);
+    } else {
+      rows_of(ru, u, a.u.st, rows, p.u_at_once);
+      if (gated) rows_of(rz, z, a.z.st, rows, p.z_at_once);
+    }
     u += TT * a.u.st, z += TT * a.z.st;
   };
   const auto write = [&](int k) {
@@ -517,7 +535,10 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
           if (gated) v = mul2(v, silu2(rz[e].pair(i)));
           o.narrow(i, v);
         }
-        if (2 * pr + e < rows) o.store(y + (long long)e * a.D, four, p.y_at_once);
+        if (wide && rows >= TT)
+          o.store(y + (long long)e * a.D, 4, 4);
+        else if (2 * pr + e < rows)
+          o.store(y + (long long)e * a.D, four, p.y_at_once);
       }
     }
     y += (long long)TT * a.D, rows -= TT;
@@ -785,6 +806,8 @@ extern "C" kda_status kda_selective_scan(const void *u, const void *delta, const
   p.C_at_once = of(Cm, 6, 4);
   p.z_at_once = z ? of(z, 8, of_group) : 1;
   p.y_at_once = of_group;
+  p.wide = p.u_at_once == 4 && p.delta_at_once == 4 && p.B_at_once == 4 && p.C_at_once == 4 &&
+           (!z || p.z_at_once == 4) && of_group == 4;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == KDA_BF16 ? launch_scan_n<__nv_bfloat16>(a, p, choice.CH, N, st)
                         : launch_scan_n<float>(a, p, choice.CH, N, st);
