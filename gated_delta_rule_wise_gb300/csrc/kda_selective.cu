@@ -196,10 +196,10 @@ template <int L> struct LaneSums {
 // fed by few warps: four recurrence warps hold the state, lanes of a channel
 // side by side; four warps turn the next tile of inputs into what the recurrence
 // reads (step sizes, dt u, B and C) in shared memory; four add D u, gate and store
-// the tile before.  A tile has one barrier.  Measured (bf16): 523 us for that
+// the tile before.  A tile has one barrier.  Measured (bf16): 516 us for that
 // prompt (4096 channels are 3.4 recurrence warps per SM, so their latency shows:
-// issue 0.59 per cycle of a busy scheduler), 201 us for 4 x 2048 tokens of 4096
-// channels (issue 0.61, shared memory 56 %, the exponential unit 33 % of its rate).
+// issue 0.58 per cycle of a busy scheduler), 189 us for 4 x 2048 tokens of 4096
+// channels (issue 0.61, shared memory 57 %, the exponential unit 35 % of its rate).
 template <typename TI, int N, int CH, bool kOut>
 __global__ void __launch_bounds__(ScanShape<TI, N, CH, kOut>::kThreads, 2)
 selective_scan_kernel(const ScanArgs a, const ScanPlan p) {

@@ -166,8 +166,8 @@ __device__ __forceinline__ void conv_token(const Taps<W, V> &taps, const Line<TI
 
 // A thread takes V channels and `run` tokens: the W - 1 inputs before them stay
 // in registers as they move along, so each input is read once but for the
-// W - 1 at a run's start.  HBM bounds it: 92 us for 32 heads x 32768 tokens x 128
-// channels in bf16, 5.8 TB/s of the 537 MB it must move (0.87 of a copy); without
+// W - 1 at a run's start.  HBM bounds it: 91 us for 32 heads x 32768 tokens x 128
+// channels in bf16, 5.9 TB/s of the 537 MB it must move (0.88 of a copy); without
 // the activation 87 us.
 template <typename TI, int W, int V>
 __global__ void __launch_bounds__(kConvThreads) short_conv_kernel(const ConvArgs a) {
