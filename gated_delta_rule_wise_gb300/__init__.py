@@ -318,6 +318,7 @@ KERNEL_SOURCES = {
     "selective_scan_kernel": ["kda_selective.cu", "kda_internal.cuh", "kda_pack.cuh"],
     "selective_step_kernel": ["kda_selective.cu", "kda_internal.cuh", "kda_pack.cuh"],
     "state_copy_kernel": ["kda_state.cu"],
+    "state_copy_ordered_kernel": ["kda_state.cu"],
     "state_clear_kernel": ["kda_state.cu"],
 }
 

@@ -488,8 +488,8 @@ kda_status kda_selective_step(const void *u, const void *delta, const float *A, 
  * effect of that order: a pair may read what an earlier one wrote, and a slot
  * may occur any number of times on either side.  src[i] == dst[i] does
  * nothing.  Pairs none of which touches what another writes (forks, moves into
- * free slots) run at once, 448 to a launch; a pair that does starts the next
- * launch.
+ * free slots) run at once, 448 to a launch; pairs that do depend on each other
+ * take more launches, or one that moves every slot's bytes in order.
  * kda_state_clear: the listed slots are filled with zero bytes.
  * layers, n_slots, n >= 0; slot_bytes >= 0; layer_stride >= n_slots *
  * slot_bytes where layers > 1.  The pool needs no alignment beyond its element;

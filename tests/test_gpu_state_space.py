@@ -360,6 +360,20 @@ def test_state_clear(shape, dtype, layered):
     assert (v[:, ~keep.cuda()] == 0).all() and (v[:, keep.cuda()] == 1).all()
 
 
+@pytest.mark.parametrize("chain", [3, 4, 5, 6, 500])
+def test_state_copy_of_few_and_many_dependent_pairs(chain):
+    """`chain` pairs that each overwrite what the one before read, after and before pairs that
+    touch nothing of theirs: on both sides of the number of launches a list may take."""
+    P = chain + 12
+    pool = torch.arange(float(P), device="cuda")[:, None].repeat(1, 20).contiguous()
+    free = chain + 1
+    src = [free] + list(range(1, chain + 1)) + [free + 1]
+    dst = [free + 2] + list(range(chain)) + [free + 3]
+    want = O.state_copy(pool.cpu().numpy()[None], src, dst)[0]
+    kda.state_copy(pool, src, dst)
+    assert np.array_equal(pool.cpu().numpy(), want)
+
+
 def test_state_copy_of_an_unaligned_pool():
     """A pool that starts one element into its storage moves in smaller pieces."""
     base = torch.arange(1 + 6 * 40, device="cuda").to(torch.bfloat16)
