@@ -15,7 +15,7 @@
 namespace kda {
 namespace {
 
-constexpr int kConvThreads = 128;
+constexpr int kConvThreads = 64;  // small, so that few are idle behind the last channel
 constexpr int kInFlight = 8;  // tokens a thread reads ahead of its products
 
 // V neighbouring channels of one token (4, 2 or 1), as loaded.  Four bf16 in eight
@@ -325,14 +325,14 @@ template <typename TI, int V> kda_status launch_conv(ConvArgs a, int W, cudaStre
   a.cx = pow2_up(C);
   a.cblocks = (C + a.cx - 1) / a.cx;
   // A run of 64 tokens reads W - 1 twice and its taps once (as many bytes as 4 to 8 tokens);
-  // shorter runs where 64 would leave SMs without eight CTAs.
+  // shorter runs where 64 would leave SMs without sixteen CTAs.
   a.run = 64;
   const auto blocks = [&] {
     const long long per = (long long)a.run * (kConvThreads / a.cx);
     a.tblocks = a.T > 0 ? (a.T + per - 1) / per : 1;
     return a.cblocks * a.tblocks * a.B;
   };
-  while (a.run > kInFlight && blocks() < 152 * 8) a.run /= 2;
+  while (a.run > kInFlight && blocks() < 152 * 16) a.run /= 2;
   const long long n = blocks();
   if (n > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
   const unsigned g = (unsigned)n;
@@ -350,8 +350,8 @@ template <typename TI, int V> kda_status launch_conv_step(ConvStepArgs a, int W,
     const long long per = (long long)a.rows * (kConvThreads / a.cx);
     return a.cblocks * ((a.N + per - 1) / per);
   };
-  a.rows = 4;  // fewer where that would leave SMs without two CTAs
-  while (a.rows > 1 && blocks() < 152 * 2) a.rows /= 2;
+  a.rows = 4;  // fewer where that would leave SMs without four CTAs
+  while (a.rows > 1 && blocks() < 152 * 4) a.rows /= 2;
   const long long n = blocks();
   if (n > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
   const unsigned g = (unsigned)n;
