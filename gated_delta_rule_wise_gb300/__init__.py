@@ -387,6 +387,7 @@ def decode_step(q, k, v, beta, log_alpha, S, stream=None):
 KDA_ACT_NONE, KDA_ACT_SILU = 0, 1
 KDA_SCAN_SOFTPLUS = 1
 _Strides10, _Strides5 = _LL * 10, _LL * 5
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _call(dev, stream, name, *args):
@@ -436,9 +437,9 @@ def _strided(t, name, shape, dtype, dev, dense=1):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, name, shape, dtype, dev)
     st = t.stride()
-    if (st[-1] != 1 and shape[-1] > 1 or
-            dense == 2 and st[-2] != shape[-1] and shape[-2] > 1) and t.numel() > 0:
-        raise ValueError(f"the last {dense} axes of {name} must be contiguous: strides {st}")
+    if st[-1] != 1 or dense == 2 and st[-2] != shape[-1]:
+        if t.numel() and (st[-1] != 1 and shape[-1] > 1 or dense == 2 and shape[-2] > 1):
+            raise ValueError(f"the last {dense} axes of {name} must be contiguous: strides {st}")
     return t.data_ptr(), st
 
 
@@ -461,9 +462,9 @@ def kda_short_conv(x, w, bias, s0, lens, y, sT, act=KDA_ACT_SILU, stream=None):
     px, st = _strided(x, "x", (B, H, T, d), dt, dev)
     state = (B, H, W - 1, d)
     _call(dev, stream, "kda_short_conv", px, st[0], st[1], st[2],
-          _dense(w, "w", (H, d, W), torch.float32, dev),
-          _dense(bias, "bias", (H, d), torch.float32, dev), _dense(s0, "s0", state, dt, dev),
-          _dense(lens, "lens", (B,), torch.int32, dev), _dense(y, "y", (B, H, T, d), dt, dev),
+          _dense(w, "w", (H, d, W), _F32, dev),
+          _dense(bias, "bias", (H, d), _F32, dev), _dense(s0, "s0", state, dt, dev),
+          _dense(lens, "lens", (B,), _I32, dev), _dense(y, "y", (B, H, T, d), dt, dev),
           _dense(sT, "sT", state, dt, dev), B, H, T, d, W, code, act)
 
 
@@ -492,10 +493,10 @@ def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
     W, P = w.shape[-1], S.shape[0]
     px, st = _strided(x, "x", (N, H, d), dt, dev)
     _call(dev, stream, "kda_short_conv_step", px, st[0], st[1],
-          _dense(w, "w", (H, d, W), torch.float32, dev),
-          _dense(bias, "bias", (H, d), torch.float32, dev),
+          _dense(w, "w", (H, d, W), _F32, dev),
+          _dense(bias, "bias", (H, d), _F32, dev),
           _dense(S, "S", (P, H, W - 1, d), dt, dev),
-          _dense(slots, "slots", (N,), torch.int32, dev), P,
+          _dense(slots, "slots", (N,), _I32, dev), P,
           _dense(y, "y", (N, H, d), dt, dev), N, H, d, W, code, act)
 
 
@@ -530,17 +531,16 @@ def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, wor
     code = _dtype_code(u)
     nB, T, nD = rows = u.shape
     G, N = B.shape[2], A.shape[1]
-    f32 = torch.float32
     pu, su = _strided(u, "u", rows, dt, dev)
     pd, sd = _strided(delta, "delta", rows, dt, dev)
     pB, sB = _strided(B, "B", (nB, T, G, N), dt, dev, 2)
     pC, sC = _strided(C, "C", (nB, T, G, N), dt, dev, 2)
     pz, sz = (None, (0, 0)) if z is None else _strided(z, "z", rows, dt, dev)
     st = _Strides10(su[0], su[1], sd[0], sd[1], sB[0], sB[1], sC[0], sC[1], sz[0], sz[1])
-    _call(dev, stream, "kda_selective_scan", pu, pd, _dense(A, "A", (nD, N), f32, dev), pB, pC,
-          _dense(D, "D", (nD,), f32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), f32, dev),
-          _dense(h0, "h0", (nB, nD, N), f32, dev), _dense(lens, "lens", (nB,), torch.int32, dev),
-          _dense(y, "y", rows, dt, dev), _dense(hT, "hT", (nB, nD, N), f32, dev), st, nB, T, nD,
+    _call(dev, stream, "kda_selective_scan", pu, pd, _dense(A, "A", (nD, N), _F32, dev), pB, pC,
+          _dense(D, "D", (nD,), _F32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), _F32, dev),
+          _dense(h0, "h0", (nB, nD, N), _F32, dev), _dense(lens, "lens", (nB,), _I32, dev),
+          _dense(y, "y", rows, dt, dev), _dense(hT, "hT", (nB, nD, N), _F32, dev), st, nB, T, nD,
           G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size())
 
@@ -570,15 +570,14 @@ def kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplu
     code = _dtype_code(u)
     R, nD = rows = u.shape
     G, N, P = B.shape[1], A.shape[1], S.shape[0]
-    f32 = torch.float32
     pu, su = _strided(u, "u", rows, dt, dev)
     pd, sd = _strided(delta, "delta", rows, dt, dev)
     pB, sB = _strided(B, "B", (R, G, N), dt, dev, 2)
     pC, sC = _strided(C, "C", (R, G, N), dt, dev, 2)
     pz, sz = (None, (0,)) if z is None else _strided(z, "z", rows, dt, dev)
-    _call(dev, stream, "kda_selective_step", pu, pd, _dense(A, "A", (nD, N), f32, dev), pB, pC,
-          _dense(D, "D", (nD,), f32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), f32, dev),
-          _dense(S, "S", (P, nD, N), f32, dev), _dense(slots, "slots", (R,), torch.int32, dev), P,
+    _call(dev, stream, "kda_selective_step", pu, pd, _dense(A, "A", (nD, N), _F32, dev), pB, pC,
+          _dense(D, "D", (nD,), _F32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), _F32, dev),
+          _dense(S, "S", (P, nD, N), _F32, dev), _dense(slots, "slots", (R,), _I32, dev), P,
           _dense(y, "y", rows, dt, dev), _Strides5(su[0], sd[0], sB[0], sC[0], sz[0]), R, nD, G,
           N, code, KDA_SCAN_SOFTPLUS if softplus else 0)
 

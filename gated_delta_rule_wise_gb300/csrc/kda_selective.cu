@@ -148,6 +148,7 @@ template <typename TI, int N, int CH, bool kOut> struct ScanShape {
   static constexpr int kBC = (kOut ? 4 : 2) * (TT / 2) * kPairBC;
   static constexpr int kY = kOut ? 2 * TT * CT * 4 : 0;
   static constexpr int kSmem = kDx + kBC + kY;
+  static_assert(kSmem <= 48 * 1024, "what a launch gets without asking");
 };
 
 // Four values v[i] summed over the L lanes of a group, one exchange per step:
@@ -458,9 +459,12 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float2 d0 = unpack(d[0][i]), d1 = unpack(d[1][i]);
-          const float2 x0 = unpack(mul2(d[0][i], ru[0].pair(i))), x1 = unpack(mul2(d[1][i], ru[1].pair(i)));
-          *reinterpret_cast<float4 *>(row + 2 * i * S::kPlane) = make_float4(d0.x, d1.x, x0.x, x1.x);
-          *reinterpret_cast<float4 *>(row + (2 * i + 1) * S::kPlane) = make_float4(d0.y, d1.y, x0.y, x1.y);
+          const float2 x0 = unpack(mul2(d[0][i], ru[0].pair(i)));
+          const float2 x1 = unpack(mul2(d[1][i], ru[1].pair(i)));
+          float4 *even = reinterpret_cast<float4 *>(row + 2 * i * S::kPlane);
+          float4 *odd = reinterpret_cast<float4 *>(row + (2 * i + 1) * S::kPlane);
+          *even = make_float4(d0.x, d1.x, x0.x, x1.x);
+          *odd = make_float4(d0.y, d1.y, x0.y, x1.y);
         }
       }
       if (has_item) {
@@ -612,7 +616,8 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Step
   f2 sum;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const f2 A0 = mul2(pack(A[q].x, A[q].y), both(kLog2e)), A1 = mul2(pack(A[q].z, A[q].w), both(kLog2e));
+    const f2 A0 = mul2(pack(A[q].x, A[q].y), both(kLog2e));
+    const f2 A1 = mul2(pack(A[q].z, A[q].w), both(kLog2e));
     const float2 e0 = unpack(exponent2(A0, step)), e1 = unpack(exponent2(A1, step));
     const f2 h0 = fma2(pack(ex2(e0.x), ex2(e0.y)), pack(s[q].x, s[q].y), mul2(xu, B[q].pair(0)));
     const f2 h1 = fma2(pack(ex2(e1.x), ex2(e1.y)), pack(s[q].z, s[q].w), mul2(xu, B[q].pair(1)));
@@ -665,26 +670,17 @@ ScanChoice scan_choice(int B, int T, int D, int G, int N, kda_dtype dt) {
   return c;
 }
 
-template <class K> bool allow_smem(K *kernel, int bytes) {  // 48 KiB need no leave
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
-             cudaSuccess;
-}
-
 template <typename TI, int N, int CH>
 kda_status launch_scan_ch(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
   using So = ScanShape<TI, N, CH, true>;
   p.tiles_g = (a.D / a.G + So::CT - 1) / So::CT;
   const long long blocks = (long long)a.B * a.G * p.tiles_g;
   if (blocks > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
-  if (!allow_smem(selective_scan_kernel<TI, N, CH, true>, So::kSmem)) return KDA_ERR_CUDA;
   if constexpr (CH == 1) {  // what scan_choice splits has one channel per lane group
     using Ss = ScanShape<TI, N, CH, false>;
-    if (p.split > 1) {
-      if (!allow_smem(selective_scan_kernel<TI, N, CH, false>, Ss::kSmem)) return KDA_ERR_CUDA;
+    if (p.split > 1)
       selective_scan_kernel<TI, N, CH, false>
           <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
-    }
   }
   selective_scan_kernel<TI, N, CH, true>
       <<<dim3((unsigned)blocks, p.split), So::kThreads, So::kSmem, st>>>(a, p);

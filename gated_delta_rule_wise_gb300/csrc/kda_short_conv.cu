@@ -147,7 +147,9 @@ template <typename TI> struct Raw<TI, 1> {
   __device__ __forceinline__ void load(const TI *q) { c = *q; }
   __device__ __forceinline__ void zero() { c = TI(0.f); }
   __device__ __forceinline__ void store(TI *q) const { *q = c; }
-  __device__ __forceinline__ void widen(Line<TI, 1> &l) const { l.p[0] = pack(Io<TI>::ld(&c), 0.f); }
+  __device__ __forceinline__ void widen(Line<TI, 1> &l) const {
+    l.p[0] = pack(Io<TI>::ld(&c), 0.f);
+  }
   __device__ __forceinline__ void narrow(const Line<TI, 1> &l) { Io<TI>::st(&c, unpack(l.p[0]).x); }
 };
 
@@ -292,7 +294,8 @@ __global__ void __launch_bounds__(kConvThreads) short_conv_step_kernel(const Con
     for (int r = 0; r < kTwo; ++r) {
       const int slot = n + r >= n1 ? -1 : a.slots ? a.slots[n + r] : n + r;
       live[r] = slot >= 0 && slot < a.n_slots;
-      S[r] = static_cast<TI *>(a.S) + ((long long)(live[r] ? slot : 0) * a.H + h) * (W - 1) * a.d + i0;
+      S[r] = static_cast<TI *>(a.S) +
+             ((long long)(live[r] ? slot : 0) * a.H + h) * (W - 1) * a.d + i0;
       if (!live[r]) continue;
 #pragma unroll
       for (int j = 0; j < W - 1; ++j) in[r][j].load(S[r] + (long long)j * a.d);
