@@ -491,13 +491,19 @@ def kda_short_conv_step(x, w, bias, S, slots, y, act=KDA_ACT_SILU, stream=None):
     code = _dtype_code(x)
     N, H, d = x.shape
     W, P = w.shape[-1], S.shape[0]
-    px, st = _strided(x, "x", (N, H, d), dt, dev)
-    _call(dev, stream, "kda_short_conv_step", px, st[0], st[1],
-          _dense(w, "w", (H, d, W), _F32, dev),
-          _dense(bias, "bias", (H, d), _F32, dev),
-          _dense(S, "S", (P, H, W - 1, d), dt, dev),
-          _dense(slots, "slots", (N,), _I32, dev), P,
-          _dense(y, "y", (N, H, d), dt, dev), N, H, d, W, code, act)
+    st = x.stride()
+    # all at once first: on a call of a few microseconds the checks are what takes time
+    if not (dt is S.dtype is y.dtype and w.dtype is _F32 and w.shape == (H, d, W)
+            and S.shape == (P, H, W - 1, d) and y.shape == x.shape
+            and dev == w.get_device() == S.get_device() == y.get_device()
+            and w.is_contiguous() and S.is_contiguous() and y.is_contiguous() and st[2] == 1):
+        _strided(x, "x", (N, H, d), dt, dev)
+        _dense(w, "w", (H, d, W), _F32, dev)
+        _dense(S, "S", (P, H, W - 1, d), dt, dev)
+        _dense(y, "y", (N, H, d), dt, dev)
+    _call(dev, stream, "kda_short_conv_step", x.data_ptr(), st[0], st[1], w.data_ptr(),
+          _dense(bias, "bias", (H, d), _F32, dev), S.data_ptr(),
+          _dense(slots, "slots", (N,), _I32, dev), P, y.data_ptr(), N, H, d, W, code, act)
 
 
 def short_conv_step(x, w, S, bias=None, slots=None, act=KDA_ACT_SILU, out=None, stream=None):
@@ -531,17 +537,27 @@ def kda_selective_scan(u, delta, A, B, C, D, z, delta_bias, h0, lens, y, hT, wor
     code = _dtype_code(u)
     nB, T, nD = rows = u.shape
     G, N = B.shape[2], A.shape[1]
-    pu, su = _strided(u, "u", rows, dt, dev)
-    pd, sd = _strided(delta, "delta", rows, dt, dev)
-    pB, sB = _strided(B, "B", (nB, T, G, N), dt, dev, 2)
-    pC, sC = _strided(C, "C", (nB, T, G, N), dt, dev, 2)
+    su, sd, sB, sC = u.stride(), delta.stride(), B.stride(), C.stride()
+    if not (dt is delta.dtype is B.dtype is C.dtype is y.dtype and A.dtype is _F32
+            and rows == delta.shape == y.shape and B.shape == C.shape == (nB, T, G, N)
+            and A.shape == (nD, N)
+            and dev == delta.get_device() == B.get_device() == C.get_device()
+            == A.get_device() == y.get_device() and A.is_contiguous() and y.is_contiguous()
+            and su[2] == sd[2] == sB[3] == sC[3] == 1 and sB[2] == sC[2] == N):
+        _strided(u, "u", rows, dt, dev)
+        _strided(delta, "delta", rows, dt, dev)
+        _strided(B, "B", (nB, T, G, N), dt, dev, 2)
+        _strided(C, "C", (nB, T, G, N), dt, dev, 2)
+        _dense(A, "A", (nD, N), _F32, dev)
+        _dense(y, "y", rows, dt, dev)
     pz, sz = (None, (0, 0)) if z is None else _strided(z, "z", rows, dt, dev)
     st = _Strides10(su[0], su[1], sd[0], sd[1], sB[0], sB[1], sC[0], sC[1], sz[0], sz[1])
-    _call(dev, stream, "kda_selective_scan", pu, pd, _dense(A, "A", (nD, N), _F32, dev), pB, pC,
-          _dense(D, "D", (nD,), _F32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), _F32, dev),
+    _call(dev, stream, "kda_selective_scan", u.data_ptr(), delta.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), _dense(D, "D", (nD,), _F32, dev), pz,
+          _dense(delta_bias, "delta_bias", (nD,), _F32, dev),
           _dense(h0, "h0", (nB, nD, N), _F32, dev), _dense(lens, "lens", (nB,), _I32, dev),
-          _dense(y, "y", rows, dt, dev), _dense(hT, "hT", (nB, nD, N), _F32, dev), st, nB, T, nD,
-          G, N, code, KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
+          y.data_ptr(), _dense(hT, "hT", (nB, nD, N), _F32, dev), st, nB, T, nD, G, N, code,
+          KDA_SCAN_SOFTPLUS if softplus else 0, _ptr(workspace),
           0 if workspace is None else workspace.numel() * workspace.element_size())
 
 
@@ -570,16 +586,28 @@ def kda_selective_step(u, delta, A, B, C, D, z, delta_bias, S, slots, y, softplu
     code = _dtype_code(u)
     R, nD = rows = u.shape
     G, N, P = B.shape[1], A.shape[1], S.shape[0]
-    pu, su = _strided(u, "u", rows, dt, dev)
-    pd, sd = _strided(delta, "delta", rows, dt, dev)
-    pB, sB = _strided(B, "B", (R, G, N), dt, dev, 2)
-    pC, sC = _strided(C, "C", (R, G, N), dt, dev, 2)
+    su, sd, sB, sC = u.stride(), delta.stride(), B.stride(), C.stride()
+    if not (dt is delta.dtype is B.dtype is C.dtype is y.dtype and _F32 is A.dtype is S.dtype
+            and rows == delta.shape == y.shape and B.shape == C.shape == (R, G, N)
+            and A.shape == (nD, N) and S.shape == (P, nD, N)
+            and dev == delta.get_device() == B.get_device() == C.get_device()
+            == A.get_device() == S.get_device() == y.get_device()
+            and A.is_contiguous() and S.is_contiguous() and y.is_contiguous()
+            and su[1] == sd[1] == sB[2] == sC[2] == 1 and sB[1] == sC[1] == N):
+        _strided(u, "u", rows, dt, dev)
+        _strided(delta, "delta", rows, dt, dev)
+        _strided(B, "B", (R, G, N), dt, dev, 2)
+        _strided(C, "C", (R, G, N), dt, dev, 2)
+        _dense(A, "A", (nD, N), _F32, dev)
+        _dense(S, "S", (P, nD, N), _F32, dev)
+        _dense(y, "y", rows, dt, dev)
     pz, sz = (None, (0,)) if z is None else _strided(z, "z", rows, dt, dev)
-    _call(dev, stream, "kda_selective_step", pu, pd, _dense(A, "A", (nD, N), _F32, dev), pB, pC,
-          _dense(D, "D", (nD,), _F32, dev), pz, _dense(delta_bias, "delta_bias", (nD,), _F32, dev),
-          _dense(S, "S", (P, nD, N), _F32, dev), _dense(slots, "slots", (R,), _I32, dev), P,
-          _dense(y, "y", rows, dt, dev), _Strides5(su[0], sd[0], sB[0], sC[0], sz[0]), R, nD, G,
-          N, code, KDA_SCAN_SOFTPLUS if softplus else 0)
+    _call(dev, stream, "kda_selective_step", u.data_ptr(), delta.data_ptr(), A.data_ptr(),
+          B.data_ptr(), C.data_ptr(), _dense(D, "D", (nD,), _F32, dev), pz,
+          _dense(delta_bias, "delta_bias", (nD,), _F32, dev), S.data_ptr(),
+          _dense(slots, "slots", (R,), _I32, dev), P, y.data_ptr(),
+          _Strides5(su[0], sd[0], sB[0], sC[0], sz[0]), R, nD, G, N, code,
+          KDA_SCAN_SOFTPLUS if softplus else 0)
 
 
 def selective_step(u, delta, A, B, C, S, D=None, z=None, delta_bias=None, slots=None,

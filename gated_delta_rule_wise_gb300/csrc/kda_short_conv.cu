@@ -119,10 +119,6 @@ template <int W, int V> struct Taps {
 template <typename TI, int V> struct Line {
   static constexpr int P = (V + 1) / 2;
   f2 p[P];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = 0;
-  }
 };
 
 template <typename TI, int V> struct Raw {  // what a load returns
