@@ -141,14 +141,22 @@ template <typename TI, int N, int CH, bool kOut> struct ScanShape {
   static constexpr int kDx = 2 * (TT / 2) * kPairRow;
   // B and C of a pair, (token 0, token 1) per n, a lane's four n in 16-byte pieces and the same
   // piece of all lanes side by side: with one channel per lane group as they are stored,
-  // since half the bytes leave shared memory then (8192 channels: 113 us, as float32 121);
+  // since half the bytes leave shared memory then (8192 channels: 110 us, as float32 121);
   // with two as float32, since the same reads serve both (193 us, widened at each use 201).
   typedef typename std::conditional<CH == 1, typename Two<TI>::raw, f2>::type bc2;
   static constexpr int kPairBC = N * (int)sizeof(bc2);
   static constexpr int kBC = (kOut ? 4 : 2) * (TT / 2) * kPairBC;
-  static constexpr int kY = kOut ? 2 * TT * CT * 4 : 0;
+  // y leaves the recurrence as sums over the lanes of a group or, with four lanes and one channel
+  // per group, as each lane's part, which the writing threads add up: fewer instructions for the
+  // recurrence, whose pace counts there (16384 tokens of 4096 channels, bf16: 464 against 519 us,
+  // float32 490 against 513; eight lanes win in bf16 what they lose in float32, two and sixteen
+  // win nothing).  A part is a float4 of four tokens; the channels lie in four planes by their
+  // last two bits, and the offsets spread what eight lanes store, two channels, over all banks.
+  static constexpr bool kParts = CH == 1 && L == 4;
+  static constexpr int kPartPlane = CT * 4 + 16, kPartLane = 4 * kPartPlane + 96;
+  static constexpr int kPartBlock = L * kPartLane;
+  static constexpr int kY = !kOut ? 0 : kParts ? 2 * (TT / 4) * kPartBlock : 2 * TT * CT * 4;
   static constexpr int kSmem = kDx + kBC + kY;
-  static_assert(kSmem <= 48 * 1024, "what a launch gets without asking");
 };
 
 // Four values v[i] summed over the L lanes of a group, one exchange per step:
@@ -197,9 +205,9 @@ template <int L> struct LaneSums {
 // fed by few warps: four recurrence warps hold the state, lanes of a channel
 // side by side; four warps turn the next tile of inputs into what the recurrence
 // reads (step sizes, dt u, B and C) in shared memory; four add D u, gate and store
-// the tile before.  A tile has one barrier.  Measured (bf16): 516 us for that
+// the tile before.  A tile has one barrier.  Measured (bf16): 464 us for that
 // prompt (4096 channels are 3.4 recurrence warps per SM, so their latency shows:
-// issue 0.58 per cycle of a busy scheduler), 189 us for 4 x 2048 tokens of 4096
+// issue 0.60 per cycle of a busy scheduler), 189 us for 4 x 2048 tokens of 4096
 // channels (issue 0.61, shared memory 57 %, the exponential unit 35 % of its rate).
 template <typename TI, int N, int CH, bool kOut>
 __global__ void __launch_bounds__(ScanShape<TI, N, CH, kOut>::kThreads, 2)
@@ -299,6 +307,8 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       // The sums over lanes of the block before run between this one's products: each
       // exchange has a quarter of a block to come back.
       LaneSums<L> sums{};
+      char *part_k = reinterpret_cast<char *>(ys) + (k & 1) * (TT / 4) * S::kPartBlock +
+                     lane * S::kPartLane + ch % 4 * S::kPartPlane + ch / 4 * 16;
       const auto store = [&](int t) {
         if (L <= 4 || lane < 4) {
 #pragma unroll
@@ -309,7 +319,8 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
         f2 s = 0;
 #pragma unroll
         for (int n = 0; n < kPer; ++n) {
-          if (kOut && n % (kPer / 2) == 0) sums.step(2 * which + n / (kPer / 2), lane);
+          if (kOut && !S::kParts && n % (kPer / 2) == 0)
+            sums.step(2 * which + n / (kPer / 2), lane);
           const float2 e = unpack(exponent2(A2[j][n], x.d[j].x));
           const float2 xb = unpack(mul2(x.d[j].y, wide(x.B[n])));
           const float h0 = fmaf(ex2(e.x), h[j][n], xb.x);
@@ -327,6 +338,11 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
       };
       const auto finish = [&](float2 a, float2 b, int t) {  // t: the block's first token
         if (!kOut) return;
+        if (S::kParts) {
+          *reinterpret_cast<float4 *>(part_k + t / 4 * S::kPartBlock) =
+              make_float4(a.x, a.y, b.x, b.y);
+          return;
+        }
         sums.step(4, lane);
         if (t > 0) store(t - TB);
         sums.v[0] = a.x, sums.v[3] = b.y;
@@ -346,7 +362,7 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
         else
           finish(y0, y1, t);
       }
-      if (kOut) {
+      if (kOut && !S::kParts) {
 #pragma unroll
         for (int s = 0; s <= 4; ++s) sums.step(s, lane);
         store(TT - TB);
@@ -528,14 +544,38 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
   };
   const auto write = [&](int k) {
     if (four > 0) {
-      const float *sy = ys + ((k & 1) * TT + 2 * pr) * CT + ch;
+      f2 s[2][2];  // [token][channels 0 and 1, 2 and 3]
+      if (S::kParts) {
+        const char *parts = reinterpret_cast<const char *>(ys) + ch / 4 * 16 + pr % 2 * 8 +
+                            ((k & 1) * (TT / 4) + pr / 2) * S::kPartBlock;
+        float2 c[4];  // a channel's two tokens
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f2 v = 0;
+#pragma unroll
+          for (int l = 0; l < L; ++l) {
+            const f2 x =
+                *reinterpret_cast<const f2 *>(parts + l * S::kPartLane + i * S::kPartPlane);
+            v = l ? add2(v, x) : x;
+          }
+          c[i] = unpack(v);
+        }
+        s[0][0] = pack(c[0].x, c[1].x), s[0][1] = pack(c[2].x, c[3].x);
+        s[1][0] = pack(c[0].y, c[1].y), s[1][1] = pack(c[2].y, c[3].y);
+      } else {
+        const float *sy = ys + ((k & 1) * TT + 2 * pr) * CT + ch;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sy + e * CT);
+          s[e][0] = v.x, s[e][1] = v.y;
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(sy + e * CT);
         Four<TI> o;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          f2 v = fma2(skip[i], ru[e].pair(i), i ? s.y : s.x);
+          f2 v = fma2(skip[i], ru[e].pair(i), s[e][i]);
           if (gated) v = mul2(v, silu2(rz[e].pair(i)));
           o.narrow(i, v);
         }
@@ -643,13 +683,13 @@ struct ScanChoice {
 // One channel per lane group, or two (half the CTAs, and half the reads of B and C per entry)?
 // An SM holds two CTAs, so a launch runs in rounds of 304 whose last is shorter where it leaves
 // one CTA to an SM.  Nanoseconds per token of a full and of such a round, measured at 8 to 64
-// states (bf16, one channel: 54 to 60 and 31; two: 88 to 110 and 60 to 70).  What it decides,
-// bf16, 16 states, 1024 tokens, one against two channels: 8192 channels 57 against 65 us,
-// 12288: 93 / 105, 16384: 118 / 105, 20480: 146 / 159.
+// states (bf16, one channel: 54 to 60 and 28 to 31; two: 88 to 110 and 60 to 70).  What it decides,
+// bf16, 16 states, 1024 tokens, one against two channels: 8192 channels 58 against 62 us,
+// 12288: 85 / 99, 16384: 109 / 100, 20480: 134 / 148.
 //
 // Where one channel per group leaves most schedulers empty, the tokens are split as well, at the
-// price of the exponentials of a second pass: 1536 channels, 8192 tokens: 6 parts 127 us, one
-// 258 us; 4096 channels, 16384 tokens: 4 parts 675 us, one 513 us, so two parts never pay.
+// price of the exponentials of a second pass: 1536 channels, 8192 tokens: 6 parts 126 us, one
+// 236 us; 4096 channels, 16384 tokens: two parts 613 us, one 466 us.
 ScanChoice scan_choice(int B, int T, int D, int G, int N, kda_dtype dt) {
   const auto rounds = [&](int CH, int full, int last) {
     const int CT = kRec / (N / kPer) * CH;
@@ -682,6 +722,10 @@ kda_status launch_scan_ch(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
       selective_scan_kernel<TI, N, CH, false>
           <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);
   }
+  if (So::kSmem > 48 * 1024 &&
+      cudaFuncSetAttribute(selective_scan_kernel<TI, N, CH, true>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, So::kSmem) != cudaSuccess)
+    return KDA_ERR_CUDA;
   selective_scan_kernel<TI, N, CH, true>
       <<<dim3((unsigned)blocks, p.split), So::kThreads, So::kSmem, st>>>(a, p);
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
