@@ -222,6 +222,21 @@ def test_scan_many_channels(B, T, D, G, N, dtype):
     _check_scan(scan_case(B, B, T, D, G, N, dtype, state=True, lens=lens), dtype)
 
 
+@pytest.mark.parametrize("lengths", ["falling", "rising", "equal", "ties", "empty"])
+@pytest.mark.parametrize("B,D,G,N,dtype", [(2, 5000, 1, 16, "bf16"), (63, 100, 1, 16, "f32"),
+                                           (64, 100, 2, 16, "bf16"), (65, 100, 1, 16, "bf16"),
+                                           (33, 260, 1, 8, "f32"), (11, 200, 1, 64, "bf16")])
+def test_scan_of_many_sequences_in_any_order(lengths, B, D, G, N, dtype):
+    """More CTAs than start at once, around the batch up to which they go by length."""
+    T = 19
+    lens = {"falling": [T - i * (T + 1) // B for i in range(B)], "equal": [T - 2] * B,
+            "rising": [i * (T + 1) // B for i in range(B)],
+            "ties": [(T, 0, 7, 7, T + 4, -2)[i % 6] for i in range(B)], "empty": [0] * B}[lengths]
+    c = scan_case(B, B, T, D, G, N, dtype, state=True, lens=lens)
+    _check_scan(c, dtype)
+    _check_scan(c, dtype, inplace=True)
+
+
 def test_scan_long_padded():
     T = 3000
     _check_scan(scan_case(3, 3, T, 16, 1, 16, "bf16", state=True, lens=[5, 1777, T]), "bf16")
@@ -593,6 +608,28 @@ def test_scan_captured_and_replayed():
     for _ in range(3):
         out.zero_()
         ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_scan_replayed_with_other_lengths():
+    """What the lengths decide is decided on the device, at each replay."""
+    B, T, D = 6, 40, 1000
+    c = scan_case(34, B, T, D, 1, 16, "bf16", state=True, lens=[T] * B)
+    t = _scan_tensors(c, "bf16", False)
+    run = lambda out: kda.selective_scan(t["u"], t["delta"], t["A"], t["Bm"], t["Cm"], t["D"],
+                                         t["z"], t["delta_bias"], t["h0"], t["lens"], out=out)
+    out = torch.zeros_like(t["u"])
+    run(out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run(out)
+    for lens in ([3, 40, 0, 39, 17, 1], [40] * B, [1, 2, 3, 4, 5, 6]):
+        t["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+        out.zero_()
+        want = run(torch.zeros_like(out))
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
