@@ -163,7 +163,8 @@ template <typename TI, int N, int CH, bool kOut> struct ScanShape {
   static constexpr int kPartPlane = CT * 4 + 16, kPartLane = 4 * kPartPlane + 96;
   static constexpr int kPartBlock = L * kPartLane;
   static constexpr int kY = !kOut ? 0 : kParts ? 2 * (TT / 4) * kPartBlock : 2 * TT * CT * 4;
-  static constexpr int kSmem = kDx + kBC + kY;
+  static constexpr int kLengths = kOut ? (kMaxByLength + 4) * 4 : 0;
+  static constexpr int kSmem = kDx + kBC + kY + kLengths;
 };
 
 // Four values v[i] summed over the L lanes of a group, one exchange per step:
@@ -228,9 +229,9 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
 
   const int tid = threadIdx.x;
   int b = blockIdx.x / (a.G * p.tiles_g);
-  if (p.by_length) {  // the sequence that b others come before; equal ones in their order
-    __shared__ __align__(16) int lens[kMaxByLength];
-    __shared__ int chosen;
+  if (kOut && p.by_length) {  // the sequence that b others come before; equal ones in their order
+    int *lens = reinterpret_cast<int *>(smem + S::kDx + S::kBC + S::kY);
+    int *chosen = lens + kMaxByLength;
     if (tid < kMaxByLength) lens[tid] = tid < a.B ? min(max(a.lens[tid], 0), a.T) : -1;
     __syncthreads();
     if (tid < a.B) {
@@ -242,10 +243,10 @@ selective_scan_kernel(const ScanArgs a, const ScanPlan p) {
         before += (v.x > mine - (j < tid)) + (v.y > mine - (j + 1 < tid)) +
                   (v.z > mine - (j + 2 < tid)) + (v.w > mine - (j + 3 < tid));
       }
-      if (before == b) chosen = tid;
+      if (before == b) *chosen = tid;
     }
     __syncthreads();
-    b = chosen;
+    b = *chosen;
   }
   const int g = blockIdx.x / p.tiles_g % a.G;
   const int per_g = a.D / a.G;
@@ -745,6 +746,7 @@ kda_status launch_scan_ch(const ScanArgs &a, ScanPlan p, cudaStream_t st) {
   p.by_length = a.lens && p.split == 1 && a.B > 1 && a.B <= kMaxByLength && blocks > 152;
   if constexpr (CH == 1) {  // what scan_choice splits has one channel per lane group
     using Ss = ScanShape<TI, N, CH, false>;
+    static_assert(Ss::kSmem <= 48 * 1024, "what a launch gets without asking");
     if (p.split > 1)
       selective_scan_kernel<TI, N, CH, false>
           <<<dim3((unsigned)blocks, p.split - 1), Ss::kThreads, Ss::kSmem, st>>>(a, p);

@@ -215,11 +215,22 @@ def test_scan_long(B, T, D, G, N, dtype):
 
 
 @pytest.mark.parametrize("B,T,D,G,N,dtype", [(40, 37, 1030, 2, 16, "bf16"), (80, 21, 640, 4, 8, "f32"),
-                                             (24, 40, 516, 3, 32, "f32"), (5, 33, 1000, 1, 64, "bf16")])
+                                             (24, 40, 516, 3, 32, "f32"), (5, 33, 1000, 1, 64, "bf16"),
+                                             (3, 50, 1000, 4, 64, "f32")])
 def test_scan_many_channels(B, T, D, G, N, dtype):
     """Enough channels that lane groups take two each; groups that end inside a CTA's channels."""
     lens = [T] + [(7 * i) % (T + 1) for i in range(1, B)]
     _check_scan(scan_case(B, B, T, D, G, N, dtype, state=True, lens=lens), dtype)
+
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scan_two_channels_per_lane_group(dtype, N, padded):
+    """Between 457 and 608 CTAs of one channel per lane group: two channels take one round."""
+    B, T, D = 4, 21, 67840 // N
+    c = scan_case(N, B, T, D, 1, N, dtype, state=True, lens=[T, 0, 9, T - 1] if padded else None)
+    _check_scan(c, dtype)
 
 
 @pytest.mark.parametrize("lengths", ["falling", "rising", "equal", "ties", "empty"])
